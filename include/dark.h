@@ -43,7 +43,7 @@
 extern "C" {
 #endif
 
-#define DARK_ABI_VERSION 6
+#define DARK_ABI_VERSION 7
 
 typedef enum {
   DARK_OK = 0,
@@ -403,6 +403,153 @@ int dark_redraw_on_forward(dark_redraw_schedule* s, int training);
 /* A manual redraw request: 1 if granted (draw advanced), else 0. */
 int dark_redraw_request(dark_redraw_schedule* s, int force);
 void dark_redraw_set_fixed(dark_redraw_schedule* s, int fixed);
+
+/*
+ * Norms of queries and keys for each head, with the position rotation in the same
+ * pass (README, section "Encoder-decoder model and generation" and the language model's
+ * rotary positions; the pages fix no norm: it is applied where a weight is given).
+ *
+ * A rotation: pairs of the first `dims` values of every head row turn by the angle
+ * position * scale * base^(-2 i / dims), i the pair's number. Pairs are (i, i + dims/2),
+ * or (2 i, 2 i + 1) when `interleaved`; values from `dims` on stay. dark_rope_init
+ * fills the struct on the host (no device work); turns[i] is the pair's frequency in
+ * 2^-64 turns a position, so that an angle is off by fp32's rounding of it (2^-25 half
+ * turns) at every position below 2^37, and repeats exactly with the position modulo 2^64.
+ * dims even, 0 <= dims <= 256 (0: no rotation), base > 0, base and scale finite.
+ */
+typedef struct dark_rope {
+  int dims, interleaved;
+  uint64_t turns[128];
+} dark_rope;
+
+dark_status dark_rope_init(dark_rope* rope, int dims, double base, double scale, int interleaved);
+
+/*
+ * Every row x (d values of one head of one token) of q and k becomes
+ *   y = rotate(x * gamma / sqrt(mean(x^2) + eps), position),
+ * sums in fp32, rounded once.
+ *   q, q_out     device [B][H][L][d] of dtype, element strides {b, h, l} (NULL =
+ *                contiguous); q_out may be q itself with the same strides
+ *   k, k_out     device [B][Hk][L][d], likewise; NULL with Hk = 0: queries only. q_out
+ *                and k_out must not overlap.
+ *   gamma_q/k    device fp32 [heads_g][d], heads_g = 1 (one weight for all heads) or the
+ *                tensor's head count; NULL: that tensor is rotated without a norm
+ *   eps          > 0 where a weight is given
+ *   rope         the rotation (host), or NULL: none
+ *   positions    device int32 [B][L], or NULL: token l is at position pos0 + l
+ * Sizes: 4 <= d <= 256, a multiple of 4; dims <= d. A row whose sum of squares passes
+ * fp32, or a non-finite result, stores DARK_ERR_NUMERIC in dev_status.
+ */
+dark_status dark_qk_norm_rope_fwd(const void* q, const int64_t* q_strides, const void* k,
+                                  const int64_t* k_strides, void* q_out,
+                                  const int64_t* q_out_strides, void* k_out,
+                                  const int64_t* k_out_strides, const float* gamma_q, int heads_gq,
+                                  const float* gamma_k, int heads_gk, float eps,
+                                  const dark_rope* rope, const int32_t* positions, int64_t pos0,
+                                  int B, int H, int Hk, int L, int d, dark_dtype dtype,
+                                  int* dev_status, void* stream);
+
+/*
+ * Backward pass of dark_qk_norm_rope_fwd: with dq_out, dk_out the gradients of its
+ * results, writes dq, dk (of dtype) and dgamma_q, dgamma_k (fp32, of the weights' shape;
+ * summed over tokens and, for a shared weight, over heads, in a fixed order). q, k are
+ * the forward's inputs. dq may be dq_out itself with the same strides (and dk dk_out);
+ * otherwise results overlap neither inputs nor each other. A weight and its gradient
+ * are both given or both NULL.
+ *   ws, ws_bytes device workspace of dark_qk_norm_rope_bwd_workspace_bytes(...) bytes,
+ *                256-byte aligned, no initial contents; one for every call in flight
+ */
+size_t dark_qk_norm_rope_bwd_workspace_bytes(int B, int H, int Hk, int L, int d);
+dark_status dark_qk_norm_rope_bwd(const void* q, const int64_t* q_strides, const void* k,
+                                  const int64_t* k_strides, const void* dq_out,
+                                  const int64_t* dq_out_strides, const void* dk_out,
+                                  const int64_t* dk_out_strides, void* dq,
+                                  const int64_t* dq_strides, void* dk, const int64_t* dk_strides,
+                                  const float* gamma_q, int heads_gq, const float* gamma_k,
+                                  int heads_gk, float* dgamma_q, float* dgamma_k, float eps,
+                                  const dark_rope* rope, const int32_t* positions, int64_t pos0,
+                                  int B, int H, int Hk, int L, int d, dark_dtype dtype, void* ws,
+                                  size_t ws_bytes, int* dev_status, void* stream);
+
+/*
+ * Paged cache of keys and values for decoding in the exact mode (README, section
+ * "Encoder-decoder model and generation": the exact mode decodes against cached keys and
+ * values). k and v are device arrays [pages][heads][page_size][d] of dtype, 16-byte
+ * aligned, owned by the caller. A sequence is a list of page numbers: its token i lies
+ * in row i % page_size of page list[i / page_size]. Keys are stored as they are (rotated,
+ * without the geometry), so a cache does not depend on a projection.
+ */
+typedef struct dark_kv_cache {
+  void *k, *v;
+  int pages, heads, page_size, d;
+  dark_dtype dtype;
+} dark_kv_cache;
+
+/*
+ * Appends up to T tokens to every sequence: token t of sequence b goes to place
+ * lens[b] + t; its key is normed (gamma_k, eps; NULL: not) and rotated (rope; NULL: not)
+ * on the way, its value copied.
+ *   k, v         device [B][heads][T][d] of the cache's dtype, strides {b, h, t} (NULL =
+ *                contiguous)
+ *   page_table   device int32 [B][max_pages]: the sequences' page lists
+ *   lens         device int32 [B]: tokens that each sequence already has (not changed)
+ *   new_lens     device int32 [B] or NULL = T: sequence b appends its first new_lens[b]
+ *                tokens (none if not positive); the others are not read
+ *   positions    device int32 [B][T], or NULL: pos0 + lens[b] + t (pos0: the length of a
+ *                prefix that is not part of the sequence's own pages)
+ * Two sequences must not name the same page where either writes. A token whose place has
+ * no page (a negative length, a place past max_pages, a page number outside the cache) is
+ * not written and stores DARK_ERR_INVALID_ARG in dev_status. Sizes as above;
+ * max_pages * page_size <= 2^30.
+ */
+dark_status dark_kv_append(const dark_kv_cache* cache, const void* k, const int64_t* k_strides,
+                           const void* v, const int64_t* v_strides, int B, int T,
+                           const int32_t* page_table, int max_pages, const int32_t* lens,
+                           const int32_t* new_lens, const float* gamma_k, int heads_gk, float eps,
+                           const dark_rope* rope, const int32_t* positions, int64_t pos0,
+                           int* dev_status, void* stream);
+
+/*
+ * Exact-mode attention of T queries of every sequence over the cache: the sequence's own
+ * tokens and a prefix that all sequences share (its keys and values are read once for
+ * the whole batch):
+ *   out = sum_j softmax_j(q^T Sigma k_j / sqrt(d)) v_j,   Sigma = M^T M of the query's head,
+ * j over the prefix's prefix_len tokens and the sequence's lens[b] own tokens. M is read
+ * from the projection's last r rows; Omega is not used. Query head h reads key head
+ * h / (H / cache->heads) (H a multiple of the cache's heads).
+ *   q, out       device [B][H][T][d] of the projection's (and cache's) dtype, strides
+ *                {b, h, t} (NULL = contiguous)
+ *   prefix_pages device int32 [ceil(prefix_len / page_size)]: the prefix's page list;
+ *                unused with prefix_len = 0
+ *   page_table   device int32 [B][max_pages]
+ *   lens         device int32 [B]: own tokens of each sequence, the T new ones included
+ *                (append them first)
+ *   flags        0: every query sees all tokens. DARK_CAUSAL: the queries are the
+ *                sequence's last T tokens, query t sees the own tokens
+ *                j <= lens[b] - T + t and the prefix; a query with lens[b] - T + t < 0 is
+ *                padding and gets a zero output. DARK_EXACT is accepted.
+ *   ws, ws_bytes device workspace of dark_cache_attention_workspace_bytes(...) bytes,
+ *                256-byte aligned, no initial contents; one for every call in flight (two
+ *                captured graphs that may run at once need two)
+ * A query that sees no token gets a zero output. Tokens behind a sequence's length, and
+ * pages that no list names, are not read into results. A length outside
+ * [0, max_pages * page_size] is clamped, and a page number outside the cache is not
+ * followed (that sequence's outputs are then unspecified); both store
+ * DARK_ERR_INVALID_ARG in dev_status. bf16 runs on the tensor cores when d is a multiple
+ * of 8: queries (after the geometry) and weights are rounded to bf16 or finer before the
+ * products, sums and softmax statistics are fp32. Every other call is computed in
+ * fp32 throughout. DARK_ERR_UNSUPPORTED: max_pages * page_size or prefix_len above 2^30,
+ * B * T above 2^20, B * H * T above 2^24, sizes outside dark_make_projection's limits.
+ */
+size_t dark_cache_attention_workspace_bytes(const dark_projection* proj, const dark_kv_cache* cache,
+                                            int B, int H, int T, int prefix_len, int max_pages);
+dark_status dark_cache_attention_fwd(const dark_projection* proj, const dark_kv_cache* cache,
+                                     const void* q, const int64_t* q_strides, void* out,
+                                     const int64_t* out_strides, int B, int H, int T,
+                                     const int32_t* prefix_pages, int prefix_len,
+                                     const int32_t* page_table, int max_pages, const int32_t* lens,
+                                     int flags, void* ws, size_t ws_bytes, int* dev_status,
+                                     void* stream);
 
 #ifdef __cplusplus
 }

@@ -368,3 +368,110 @@ def uses_exact(L: int, exact_threshold: int) -> bool:
     """Auto mode (README, "Attention modes"): the exact mode for sequences up
     to the threshold length, random features for longer ones."""
     return exact_threshold > 0 and L <= exact_threshold
+
+
+# ------------------------------------------- head norms, rotation, paged cache --
+#
+# README, section "Attention modes" (exact mode) and "Encoder-decoder model and
+# generation" (the exact mode decodes against cached keys and values). The pages fix
+# neither a norm of the heads nor a cache layout; the formulas are those of the
+# public header's comments.
+
+def _angles(positions, dims, base, scale):
+    """Angles [..., dims / 2] of the pairs at the positions [...]."""
+    i = np.arange(dims // 2, dtype=np.float64)
+    f = scale * base ** (-2.0 * i / max(dims, 1))
+    return np.asarray(positions, np.float64)[..., None] * f
+
+
+def _pair_index(dims, interleaved):
+    """Columns of the pairs' first and second values."""
+    half = dims // 2
+    if interleaved:
+        return np.arange(0, dims, 2), np.arange(1, dims, 2)
+    return np.arange(half), np.arange(half, dims)
+
+
+def rotate(x, positions, dims, base=10000.0, scale=1.0, interleaved=False, transpose=False):
+    """x [B, H, L, d] with the pairs of its first `dims` values turned by the angles of
+    positions [B, L] (or back, with `transpose`)."""
+    x = _f64(x).copy()
+    if dims == 0:
+        return x
+    t = _angles(positions, dims, base, scale)[:, None]
+    c, s = np.cos(t), np.sin(t) * (-1.0 if transpose else 1.0)
+    ia, ib = _pair_index(dims, interleaved)
+    a, b = x[..., ia], x[..., ib]
+    x[..., ia], x[..., ib] = a * c - b * s, a * s + b * c
+    return x
+
+
+def norm_rope(x, gamma, eps, positions, dims, base=10000.0, scale=1.0, interleaved=False):
+    """rotate(x gamma / sqrt(mean(x^2) + eps)): x [B, H, L, d], gamma [1 or H, d] or None."""
+    x = _f64(x)
+    if gamma is not None:
+        x = x / np.sqrt((x * x).mean(-1, keepdims=True) + eps) * _f64(gamma)[None, :, None, :]
+    return rotate(x, positions, dims, base, scale, interleaved)
+
+
+def norm_rope_backward(x, gamma, eps, positions, dy, dims, base=10000.0, scale=1.0,
+                       interleaved=False):
+    """Gradients (dx, dgamma) of sum(dy * norm_rope(x, ...)); dgamma None without a gamma."""
+    x = _f64(x)
+    u = rotate(dy, positions, dims, base, scale, interleaved, transpose=True)
+    if gamma is None:
+        return u, None
+    rstd = 1.0 / np.sqrt((x * x).mean(-1, keepdims=True) + eps)
+    n = x * rstd
+    w = u * _f64(gamma)[None, :, None, :]
+    dx = rstd * (w - n * (w * n).mean(-1, keepdims=True))
+    dg = (u * n).sum(axis=(0, 2))
+    return dx, dg if len(gamma) > 1 or x.shape[1] == 1 else dg.sum(0, keepdims=True)
+
+
+def kv_append(k_pages, v_pages, k, v, page_table, lens, new_lens=None):
+    """The pools [pages, heads, page_size, d] with token t of sequence b of k, v [B, heads, T, d]
+    at place lens[b] + t of its page list, for t < new_lens[b] (all T without)."""
+    k_pages, v_pages = _f64(k_pages).copy(), _f64(v_pages).copy()
+    page = k_pages.shape[2]
+    for b in range(k.shape[0]):
+        for t in range(k.shape[2] if new_lens is None else min(int(new_lens[b]), k.shape[2])):
+            at = int(lens[b]) + t
+            p = page_table[b][at // page]
+            k_pages[p, :, at % page] = k[b, :, t]
+            v_pages[p, :, at % page] = v[b, :, t]
+    return k_pages, v_pages
+
+
+def cache_rows(pages, page_list, count, h):
+    """The first `count` rows of key head h along a list of pages."""
+    page = pages.shape[2]
+    return _f64(np.array([pages[page_list[j // page], h, j % page] for j in range(count)]
+                         ).reshape(count, pages.shape[3]))
+
+
+def cache_attention(q, k_pages, v_pages, geom, page_table, lens, prefix_pages=None, prefix_len=0,
+                    causal=False):
+    """Exact-mode attention of q [B, H, T, d] over the prefix's tokens and each sequence's
+    lens[b] own tokens. Causal: query t sees the own tokens j <= lens[b] - T + t and the
+    prefix; with lens[b] - T + t < 0 it is padding. Rows that see nothing are 0."""
+    q = _f64(q)
+    B, H, T, d = q.shape
+    group = H // k_pages.shape[1]
+    out = np.zeros((B, H, T, d))
+    for b in range(B):
+        n = int(lens[b])
+        for h in range(H):
+            rows = [(prefix_pages, prefix_len), (page_table[b], n)]
+            k, v = (np.concatenate([cache_rows(x, p, c, h // group) for p, c in rows if c]
+                                   or [np.zeros((0, d))]) for x in (k_pages, v_pages))
+            m = _f64(_head(geom, h)) * d ** -0.25
+            scores = (q[b, h] @ m.T) @ (k @ m.T).T
+            for t in range(T):
+                see = prefix_len + (n - T + t + 1 if causal else n)
+                if see <= 0 or (causal and n - T + t < 0):
+                    continue
+                z = scores[t, :see]
+                p = np.exp(z - z.max())
+                out[b, h, t] = (p / p.sum()) @ v[:see]
+    return out

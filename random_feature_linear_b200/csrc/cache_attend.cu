@@ -1,0 +1,466 @@
+// Exact-mode attention of T queries of every sequence over a paged cache, for a batch
+// whose sequences share one prefix (README, section "Attention modes": in the exact
+// mode M acts on queries and keys and ordinary softmax attention follows; section
+// "Encoder-decoder model and generation": the exact mode decodes against cached keys
+// and values).
+//
+// The cache holds keys as they are, so the geometry goes to the query's side:
+//   y = log2(e) M^T M q / sqrt(d),  s_j = y . k_j,  out = sum_j 2^(s_j - m) v_j / sum_j 2^(s_j - m).
+// Three launches: the queries y with the cut of the own keys into ranges (lengths are
+// known on the device only); partial sums of every range (prefix ranges hold the rows of
+// the whole batch, so the prefix is read once for all sequences); the join.
+//
+// This file: the first and last launch, the plan, and the fp32 kernel of the ranges,
+// which takes every type, size and layout. bf16 rows of 16-byte multiples take the
+// tensor-core kernels.
+#include <math.h>
+#include <string.h>
+
+#include "cache_attend.cuh"
+#include "cache_attend_mma.cuh"
+#include "tc_common.cuh"
+
+namespace dark {
+namespace cache {
+namespace {
+
+constexpr int kPrepRows = 8;
+
+// ------------------------------------------------- queries and the cut of keys --
+
+// The cut of the own keys: ranges of `chunk` keys, as short as `cap` ranges allow (so
+// that a few long sequences spread over the GPU too).
+__device__ void make_sched(const Params& q) {
+  __shared__ int part[33];
+  __shared__ long long wsum[32];
+  __shared__ int chunk_s;
+  Sched* sc = at<Sched>(q.a, q.p.o_sched);
+  int* off = sched_off(sc);
+  int* len = sched_len(sc, q.a.B);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x / 32;
+  const int64_t most = (int64_t)q.a.max_pages * q.a.page;
+  long long sum = 0;
+  for (int b = tid; b < q.a.B; b += blockDim.x) {
+    int64_t n = q.a.lens[b];
+    if (n < 0 || n > most) {
+      report(q.a.dev_status, DARK_ERR_INVALID_ARG);
+      n = n < 0 ? 0 : most;
+    }
+    len[b] = (int)n;
+    sum += n;
+  }
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) wsum[warp] = sum;
+  __syncthreads();
+  if (tid == 0) {
+    long long all = 0;
+    for (int w = 0; w < nw; ++w) all += wsum[w];
+    // sum ceil(len / chunk) <= all / chunk + B <= cap
+    const long long room = q.p.cap - q.a.B > 0 ? q.p.cap - q.a.B : 1;
+    long long c = (all + room - 1) / room;
+    c = (c + kKeyStep - 1) / kKeyStep * kKeyStep;
+    // no sequence is longer than 2^30 keys: longer ranges change nothing
+    chunk_s = c < 2 * kKeyStep ? 2 * kKeyStep : c < (1 << 30) ? (int)c : 1 << 30;
+  }
+  __syncthreads();
+  const int chunk = chunk_s;
+  int base = 0;
+  for (int b0 = 0; b0 < q.a.B; b0 += blockDim.x) {
+    const int b = b0 + tid;
+    const int n = b < q.a.B ? (int)(((long long)len[b] + chunk - 1) / chunk) : 0;
+    int x = n;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) part[warp] = x;
+    __syncthreads();
+    int before = base;
+    for (int w = 0; w < warp; ++w) before += part[w];
+    if (b < q.a.B) off[b] = before + x - n;
+    int all = 0;
+    for (int w = 0; w < nw; ++w) all += part[w];
+    base += all;
+    __syncthreads();
+  }
+  if (tid == 0) {
+    off[q.a.B] = base;
+    sc->chunk = chunk;
+    sc->total = base;
+  }
+}
+
+// y of kPrepRows rows of one query head: p = (c_m M) q, y = 2 (c_m M)^T p. Threads over
+// the rows of M, then over the columns; sums in fp32.
+template <typename T>
+__global__ void __launch_bounds__(256) queries_kernel(const __grid_constant__ Params q) {
+  using W = typename WeightOf<T>::type;
+  if (blockIdx.x == gridDim.x - 1) {
+    if (blockIdx.y == 0) make_sched(q);
+    return;
+  }
+  extern __shared__ float sm[];
+  const int d = q.a.d, r = q.a.r, tid = threadIdx.x;
+  float* x = sm;                          // [d][kPrepRows]
+  float* p = sm + kPrepRows * d;          // [r][kPrepRows]
+  const int h = blockIdx.y, n0 = blockIdx.x * kPrepRows;     // rows (b, t) of head h
+  const int n = q.a.B * q.a.T;
+  const W* w = (const W*)q.a.w + ((int64_t)(q.a.heads_w == 1 ? 0 : h) * (q.a.m + r) + q.a.m) * d;
+  for (int i = tid; i < kPrepRows * d; i += blockDim.x) {
+    const int row = i / d, c = i - row * d, k = n0 + row;
+    float v = 0.f;
+    if (k < n) {
+      const int b = k / q.a.T, t = k - b * q.a.T;
+      v = to_f32(((const T*)q.a.q)[b * q.a.qs[0] + h * q.a.qs[1] + t * q.a.qs[2] + c]);
+    }
+    x[c * kPrepRows + row] = v;
+  }
+  __syncthreads();
+  for (int i = tid; i < r; i += blockDim.x) {
+    float s[kPrepRows];
+#pragma unroll
+    for (int k = 0; k < kPrepRows; ++k) s[k] = 0.f;
+    for (int c = 0; c < d; ++c) {
+      const float u = to_f32(w[(int64_t)i * d + c]);
+#pragma unroll
+      for (int k = 0; k < kPrepRows; ++k) s[k] = fmaf(u, x[c * kPrepRows + k], s[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kPrepRows; ++k) p[i * kPrepRows + k] = 2.f * s[k];
+  }
+  __syncthreads();
+  const int g = h % q.G, hk = h / q.G, dp = q.p.dp;
+  for (int c = tid; c < dp; c += blockDim.x) {
+    float s[kPrepRows];
+#pragma unroll
+    for (int k = 0; k < kPrepRows; ++k) s[k] = 0.f;
+    if (c < d)
+      for (int i = 0; i < r; ++i) {
+        const float u = to_f32(w[(int64_t)i * d + c]);
+#pragma unroll
+        for (int k = 0; k < kPrepRows; ++k) s[k] = fmaf(u, p[i * kPrepRows + k], s[k]);
+      }
+    for (int k = 0; k < kPrepRows && n0 + k < n; ++k) {
+      const int b = (n0 + k) / q.a.T, t = (n0 + k) - b * q.a.T;
+      const int64_t row = (int64_t)hk * q.p.all + (b * q.G + g) * q.a.T + t;
+      if (q.p.mma)
+        store_query_hi_lo(at<__nv_bfloat16>(q.a, q.p.o_y), (int64_t)q.a.Hk * q.p.all, row, dp, c, s[k]);
+      else
+        at<float>(q.a, q.p.o_y)[row * dp + c] = s[k];
+    }
+  }
+}
+
+// ------------------------------------------------------ ranges in fp32 (SIMT) --
+
+// RB rows against one key range, KT keys at a time: 128 threads as RB / 4 row groups of
+// four rows. Scores and sums are register tiles of four rows (by 1-2 keys, by up to 16
+// columns); the running exponent and weight of a row live in shared memory. Bound by
+// fp32 multiply-adds for many rows, by the key and value rows for few.
+template <typename T, int RB, int KT>
+__global__ void __launch_bounds__(128) range_kernel(const __grid_constant__ Params q, int prefix) {
+  constexpr int RG = RB / 4, CG = 128 / RG, KJ = KT / CG, NJ = (256 + 4 * CG - 1) / (4 * CG);
+  static_assert(KT % CG == 0, "keys over column groups");
+  const int hk = blockIdx.y;
+  const Item it = item_of(q, blockIdx.x, hk, RB, prefix != 0, prefix == 0);
+  if (!it.any) return;
+  extern __shared__ __align__(16) float sm[];
+  const int d = q.a.d, ld = d + 4, tid = threadIdx.x;
+  float* ys = sm;                         // [RB][ld]
+  float* kv = ys + RB * ld;               // [KT][ld]: keys, then values
+  float* sc = kv + KT * ld;               // [KT][RB + 4]: scores, then weights
+  float* mx = sc + KT * (RB + 4);         // [RB] reference exponent
+  float* lw = mx + RB;                    // [RB] weight
+  float* fac = lw + RB;                   // [RB] factor of the sums so far
+  int* lim = (int*)(fac + RB);            // [RB] visible keys
+  const float* y = at<float>(q.a, q.p.o_y) + ((int64_t)hk * q.p.all + it.row0) * q.p.dp;
+  for (int i = tid; i < RB * d; i += 128) {
+    const int row = i / d, c = i - row * d;
+    ys[row * ld + c] = row < it.nrows ? y[(int64_t)row * q.p.dp + c] : 0.f;
+  }
+  if (tid < RB) {
+    mx[tid] = -INFINITY;
+    lw[tid] = 0.f;
+    lim[tid] = tid < it.nrows ? visible_keys(q, it, tid) : 0;
+  }
+  const int rg = tid / CG, cg = tid % CG;
+  float acc[4][NJ][4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[r][j][e] = 0.f;
+
+  auto fill = [&](const void* pool, int j0) {          // KT rows; zeros past the range
+    const int per = d / 4;
+    for (int i = tid; i < KT * per; i += 128) {
+      const int k = i / per, c = (i - k * per) * 4;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (j0 + k < it.k1) {
+        const int64_t row = cache_row(q.a, it.pages, j0 + k, hk);
+        if (row >= 0) {
+          const T* src = (const T*)pool + row * d + c;
+          if constexpr (sizeof(T) == 4) {
+            v = *reinterpret_cast<const float4*>(src);
+          } else {
+            v = make_float4(to_f32(src[0]), to_f32(src[1]), to_f32(src[2]), to_f32(src[3]));
+          }
+        } else {
+          report(q.a.dev_status, DARK_ERR_INVALID_ARG);
+        }
+      }
+      *reinterpret_cast<float4*>(kv + k * ld + c) = v;
+    }
+  };
+
+  for (int j0 = it.k0; j0 < it.k1; j0 += KT) {
+    __syncthreads();                                   // the last tile's readers are done
+    fill(q.a.kp, j0);
+    __syncthreads();
+    float s[4][KJ];
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int k = 0; k < KJ; ++k) s[r][k] = 0.f;
+    for (int c = 0; c < d; c += 4) {
+      float4 a[4], b[KJ];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) a[r] = *reinterpret_cast<const float4*>(ys + (rg * 4 + r) * ld + c);
+#pragma unroll
+      for (int k = 0; k < KJ; ++k) b[k] = *reinterpret_cast<const float4*>(kv + (cg + k * CG) * ld + c);
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int k = 0; k < KJ; ++k) {
+          s[r][k] = fmaf(a[r].x, b[k].x, s[r][k]);
+          s[r][k] = fmaf(a[r].y, b[k].y, s[r][k]);
+          s[r][k] = fmaf(a[r].z, b[k].z, s[r][k]);
+          s[r][k] = fmaf(a[r].w, b[k].w, s[r][k]);
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int k = 0; k < KJ; ++k) {
+        const int key = j0 + cg + k * CG, row = rg * 4 + r;
+        sc[(cg + k * CG) * (RB + 4) + row] = key < it.k1 && key < lim[row] ? s[r][k] : -INFINITY;
+      }
+    __syncthreads();
+    fill(q.a.vp, j0);
+    // a warp takes rows warp, warp + 4, ...: exponent, weights, factor
+    for (int row = tid >> 5; row < RB; row += 4) {
+      float top = -INFINITY;
+      for (int k = tid & 31; k < KT; k += 32) top = fmaxf(top, sc[k * (RB + 4) + row]);
+      top = warp_max(top);
+      const float old = mx[row], now = fmaxf(old, top), ref = now == -INFINITY ? 0.f : now;
+      float sum = 0.f;
+      for (int k = tid & 31; k < KT; k += 32) {
+        const float p = exp2f(sc[k * (RB + 4) + row] - ref);
+        sc[k * (RB + 4) + row] = p;
+        sum += p;
+      }
+      sum = warp_sum(sum);
+      if ((tid & 31) == 0) {
+        const float f = exp2f(old - ref);              // 0 before the first visible key
+        fac[row] = f;
+        lw[row] = fmaf(lw[row], f, sum);
+        mx[row] = now;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float f = fac[rg * 4 + r];
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[r][j][e] *= f;
+    }
+    const int nk = it.k1 - j0 < KT ? it.k1 - j0 : KT;
+    int all = nk;                                      // keys that all four rows see
+#pragma unroll
+    for (int r = 0; r < 4; ++r) all = min(all, lim[rg * 4 + r] - j0);
+    for (int k = 0; k < nk; ++k) {
+      const float4 p = *reinterpret_cast<const float4*>(sc + k * (RB + 4) + rg * 4);
+      const float pr[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const int c = (cg + j * CG) * 4;
+        if (c < d) {
+          const float4 v = *reinterpret_cast<const float4*>(kv + k * ld + c);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            // a weight of 0 does not cancel an infinite or NaN value behind the mask
+            if (k >= all && j0 + k >= lim[rg * 4 + r]) continue;
+            acc[r][j][0] = fmaf(pr[r], v.x, acc[r][j][0]);
+            acc[r][j][1] = fmaf(pr[r], v.y, acc[r][j][1]);
+            acc[r][j][2] = fmaf(pr[r], v.z, acc[r][j][2]);
+            acc[r][j][3] = fmaf(pr[r], v.w, acc[r][j][3]);
+          }
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int row = rg * 4 + r;
+    if (row >= it.nrows) continue;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const int c = (cg + j * CG) * 4;
+      if (c < d)
+        *reinterpret_cast<float4*>(it.acc + (int64_t)row * d + c) =
+            make_float4(acc[r][j][0], acc[r][j][1], acc[r][j][2], acc[r][j][3]);
+    }
+    if (cg == 0) {
+      it.ml[2 * row] = mx[row];
+      it.ml[2 * row + 1] = lw[row];
+    }
+  }
+}
+
+// -------------------------------------------------------------------- the join --
+
+// One warp a row: out = sum_i 2^(m_i - m) acc_i / sum_i 2^(m_i - m) l_i over the row's
+// prefix and own ranges, in their order. Rows that see no key give zeros.
+template <typename T>
+__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Params q) {
+  const int lane = threadIdx.x & 31;
+  const int64_t n = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (n >= (int64_t)q.a.Hk * q.p.all) return;
+  const int hk = (int)(n / q.p.all), row = (int)(n - (int64_t)hk * q.p.all);
+  const int b = row / q.p.rows, in = row - b * q.p.rows, g = in / q.a.T, t = in - g * q.a.T;
+  Sched* sc = at<Sched>(q.a, q.p.o_sched);
+  const int len = sched_len(sc, q.a.B)[b], r0 = sched_off(sc)[b], r1 = sched_off(sc)[b + 1];
+  const bool pad = (q.a.flags & DARK_CAUSAL) && len - q.a.T + t < 0;
+  const int d = q.a.d, np = q.a.prefix_len > 0 && !pad ? q.p.p_splits : 0, no = pad ? 0 : r1 - r0;
+  const float* pml = at<float>(q.a, q.p.o_pml) + ((size_t)hk * q.p.p_splits * q.p.all + row) * 2;
+  const float* oml = at<float>(q.a, q.p.o_oml) + (((size_t)hk * q.p.cap + r0) * q.p.rows + in) * 2;
+  auto ml = [&](int i) {
+    return *reinterpret_cast<const float2*>(i < np ? pml + (size_t)i * q.p.all * 2
+                                                   : oml + (size_t)(i - np) * q.p.rows * 2);
+  };
+  float top = -INFINITY;
+  for (int i = lane; i < np + no; i += 32) top = fmaxf(top, ml(i).x);
+  top = warp_max(top);
+  const float ref = top == -INFINITY ? 0.f : top;
+  const float* pa = at<float>(q.a, q.p.o_pacc) + ((size_t)hk * q.p.p_splits * q.p.all + row) * d;
+  const float* oa = at<float>(q.a, q.p.o_oacc) + (((size_t)hk * q.p.cap + r0) * q.p.rows + in) * d;
+  float l = 0.f, o[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) o[j] = 0.f;
+  for (int i = 0; i < np + no; ++i) {
+    const float2 v = ml(i);
+    const float f = exp2f(v.x - ref);
+    l = fmaf(f, v.y, l);
+    if (f == 0.f) continue;                            // no visible key: acc is not read
+    const float* src = i < np ? pa + (size_t)i * q.p.all * d : oa + (size_t)(i - np) * q.p.rows * d;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (lane + 32 * j < d) o[j] = fmaf(f, src[lane + 32 * j], o[j]);
+  }
+  T* dst = (T*)q.a.out + b * q.a.os[0] + (int64_t)(hk * q.G + g) * q.a.os[1] + t * q.a.os[2];
+  bool bad = false;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (lane + 32 * j >= d) continue;
+    const float v = l == 0.f ? 0.f : o[j] / l;
+    bad |= !isfinite(v);
+    dst[lane + 32 * j] = from_f32<T>(v);
+  }
+  if (bad) report(q.a.dev_status, DARK_ERR_NUMERIC);
+}
+
+// -------------------------------------------------------------------- the plan --
+
+int row_block(const Plan& p, int rows) {
+  if (p.mma) return mma_rows(p.dp, p.rows);
+  return rows >= 32 ? 32 : 8;
+}
+
+Plan make_plan(const CacheAttnArgs& a) {
+  Plan p;
+  memset(&p, 0, sizeof(p));
+  p.rows = a.H / a.Hk * a.T;
+  p.all = a.B * p.rows;
+  p.mma = a.dtype == DARK_BF16 && a.d % 8 == 0;
+  p.dp = p.mma ? (a.d <= 64 ? 64 : a.d <= 128 ? 128 : 256) : a.d;
+  // ranges: about four CTAs an SM over key heads, row blocks and ranges
+  const long long want = 4LL * 148;
+  const long long pb = (long long)a.Hk * ((p.all + row_block(p, p.all) - 1) / row_block(p, p.all));
+  const int steps = (a.prefix_len + kKeyStep - 1) / kKeyStep;
+  long long s = (want + pb - 1) / pb;
+  if (s > (steps + 1) / 2) s = (steps + 1) / 2;
+  if (s < 1) s = 1;
+  p.p_chunk = steps == 0 ? kKeyStep : (int)((steps + s - 1) / s * kKeyStep);
+  p.p_splits = steps == 0 ? 1 : (a.prefix_len + p.p_chunk - 1) / p.p_chunk;
+  const long long ob = (long long)a.Hk * ((p.rows + row_block(p, p.rows) - 1) / row_block(p, p.rows));
+  p.cap = a.B + (int)((want + ob - 1) / ob);
+  size_t o = kWsHeader;
+  auto take = [&](size_t n) {
+    const size_t at = o;
+    o += align_up(n, 256);
+    return at;
+  };
+  const size_t krows = (size_t)a.Hk * p.all;
+  p.o_sched = take(sizeof(Sched) + (size_t)(2 * a.B + 1) * 4);
+  p.o_y = take(krows * p.dp * 4);
+  p.o_pacc = take(a.prefix_len > 0 ? krows * p.p_splits * a.d * 4 : 0);
+  p.o_pml = take(a.prefix_len > 0 ? krows * p.p_splits * 8 : 0);
+  p.o_oacc = take((size_t)a.Hk * p.cap * p.rows * a.d * 4);
+  p.o_oml = take((size_t)a.Hk * p.cap * p.rows * 8);
+  p.bytes = o;
+  return p;
+}
+
+template <typename T, int RB, int KT>
+cudaError_t launch_range(const Params& q, bool prefix) {
+  static int smem_set[64];
+  const int d = q.a.d;
+  const size_t smem = ((size_t)(RB + KT) * (d + 4) + (size_t)KT * (RB + 4) + 4 * RB) * 4;
+  const size_t most = ((size_t)(RB + KT) * 260 + (size_t)KT * (RB + 4) + 4 * RB) * 4;
+  cudaError_t e = set_smem_limit_once((const void*)range_kernel<T, RB, KT>, (int)most, smem_set);
+  if (e != cudaSuccess) return e;
+  const int rows = prefix ? q.p.all : q.p.rows;
+  const long long n = (long long)(prefix ? q.p.p_splits : q.p.cap) * ((rows + RB - 1) / RB);
+  range_kernel<T, RB, KT><<<dim3((unsigned)n, q.a.Hk), 128, smem, q.a.stream>>>(q, prefix ? 1 : 0);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_all(const Params& q) {
+  const int n = q.a.B * q.a.T;
+  const size_t smem = (size_t)kPrepRows * (q.a.d + q.a.r) * 4;
+  queries_kernel<T><<<dim3((n + kPrepRows - 1) / kPrepRows + 1, q.a.H), 256, smem, q.a.stream>>>(q);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  if (q.p.mma) {
+    e = launch_ranges_mma(q);
+    if (e != cudaSuccess) return e;
+  } else {
+    for (int prefix = q.a.prefix_len > 0 ? 1 : 0; prefix >= 0; --prefix) {
+      const int rows = prefix ? q.p.all : q.p.rows;
+      e = rows >= 32 ? launch_range<T, 32, 32>(q, prefix != 0) : launch_range<T, 8, 64>(q, prefix != 0);
+      if (e != cudaSuccess) return e;
+    }
+  }
+  const int64_t rows = (int64_t)q.a.Hk * q.p.all;
+  join_kernel<T><<<(unsigned)((rows + 3) / 4), 128, 0, q.a.stream>>>(q);
+  return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace cache
+
+size_t cache_attention_workspace_bytes(const CacheAttnArgs& a) { return cache::make_plan(a).bytes; }
+
+cudaError_t launch_cache_attention(const CacheAttnArgs& a) {
+  cache::Params q;
+  q.a = a;
+  q.p = cache::make_plan(a);
+  q.G = a.H / a.Hk;
+  return a.dtype == DARK_BF16 ? cache::launch_all<__nv_bfloat16>(q) : cache::launch_all<float>(q);
+}
+
+}  // namespace dark

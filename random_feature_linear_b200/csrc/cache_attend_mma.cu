@@ -1,0 +1,350 @@
+// Cache attention, key ranges on the tensor cores for few rows (bf16).
+//
+// A CTA of four warps takes one key range and a block of 8 or 16 rows. Every warp
+// streams its own tiles of 16 keys (tiles w, w + 4, ...) through a private ring in
+// shared memory (cp.async, 16 bytes a lane, no barrier between warps) and keeps its own
+// reference exponents, weights and sums; the four are joined once at the end.
+//
+// mma.sync m16n8k16 has 16 rows; eight queries fill it twice, as y = hi + lo: rows 0-7
+// hold hi, rows 8-15 lo, and a thread's accumulators of rows g and g + 8 add up to the
+// score. The weights P = hi + lo go the same way, so both products keep 16 bits of
+// significand at the price of one product with 16 rows. A row's reference exponent only
+// moves when a score passes it by 2^8 (sums and weights stay far inside fp32), so that
+// sums are rescaled a few times a range instead of every tile.
+//
+// Bound by the key and value rows (read once for all rows of the block): 4 d bytes a key.
+#include <math.h>
+
+#include "cache_attend_mma.cuh"
+#include "tc_common.cuh"
+
+namespace dark {
+namespace cache {
+namespace {
+
+constexpr int kWarps = 4, kKeys = 16;
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Byte offset of 16-byte chunk `c` of row `row` in a tile of DP bf16 columns: chunks
+// XORed with the row's low bits, so that eight rows at one chunk hit eight bank groups.
+template <int DP>
+__device__ __forceinline__ uint32_t tile_off(int row, int c) {
+  return (uint32_t)(row * DP * 2 + ((c ^ (row & 7)) << 4));
+}
+
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float bf16_half(uint32_t w, int upper) {
+  return __uint_as_float(upper ? w & 0xffff0000u : w << 16);
+}
+// Whether a tile of kKeys rows holds an infinity or NaN (the same answer in all lanes).
+template <int DP>
+__device__ __forceinline__ bool tile_non_finite(uint32_t tile, int lane) {
+  bool bad = false;
+  for (int n = lane; n < kKeys * DP / 8; n += 32) {
+    const uint4 w = tc::ld_shared_v4(tile + 16 * n);
+    for (uint32_t x : {w.x, w.y, w.z, w.w})
+      bad |= (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
+  }
+  return __any_sync(0xffffffffu, bad);
+}
+
+template <int DP>
+struct Cfg {
+  static constexpr uint32_t kTile = kKeys * DP * 2;       // one matrix of a tile
+  static constexpr int kStages = DP == 64 ? 6 : 3;
+  static constexpr uint32_t kWarpBytes = kStages * 2 * kTile;
+  static constexpr uint32_t kSmem = kWarps * kWarpBytes;
+};
+
+// RT: row tiles of eight rows.
+template <int DP, int RT>
+__global__ void __launch_bounds__(kWarps * 32) range_mma_kernel(const __grid_constant__ Params q) {
+  using C = Cfg<DP>;
+  constexpr int NS = DP / 16, NT = DP / 8;                // k-steps of a score, column tiles
+  constexpr int RB = 8 * RT, S = C::kStages;
+  const int hk = blockIdx.y;
+  const Item it = item_of(q, blockIdx.x, hk, RB, q.a.prefix_len > 0, true);
+  if (!it.any) return;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  uint8_t* ring = smem + warp * C::kWarpBytes;
+  const uint32_t ring0 = tc::smem_u32(ring);
+  const int d = q.a.d, chunks = d / 8;
+  const __nv_bfloat16* kp = (const __nv_bfloat16*)q.a.kp;
+  const __nv_bfloat16* vp = (const __nv_bfloat16*)q.a.vp;
+
+  // rows of the cache that this warp's tile i holds, one key a lane (lanes 0-15)
+  const int ntiles = (it.k1 - it.k0 + kKeys - 1) / kKeys;
+  const int mine = ntiles > warp ? (ntiles - warp + kWarps - 1) / kWarps : 0;
+  auto lookup = [&](int i) -> int64_t {
+    const int key = it.k0 + (warp + i * kWarps) * kKeys + (lane & 15);
+    if (i >= mine || key >= it.k1) return -1;
+    const int64_t row = cache_row(q.a, it.pages, key, hk);
+    if (row < 0) report(q.a.dev_status, DARK_ERR_INVALID_ARG);
+    return row;
+  };
+  auto issue = [&](int i, int64_t row) {                  // zeros past the range and past d
+    const uint32_t k0 = ring0 + (uint32_t)(i % S) * 2 * C::kTile, v0 = k0 + C::kTile;
+    constexpr int CH = DP / 8;
+#pragma unroll
+    for (int n = 0; n < kKeys * CH / 32; ++n) {
+      const int idx = n * 32 + lane, r = idx / CH, c = idx % CH;
+      const int64_t at = __shfl_sync(0xffffffffu, row, r);
+      const bool ok = at >= 0 && c < chunks;
+      const int64_t o = ok ? at * d + c * 8 : 0;
+      cp16(k0 + tile_off<DP>(r, c), kp + o, ok);
+      cp16(v0 + tile_off<DP>(r, c), vp + o, ok);
+    }
+  };
+  int64_t next = lookup(0);
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) {
+    const int64_t row = next;
+    next = lookup(i + 1);
+    if (i < mine) issue(i, row);
+    cp_commit();
+  }
+
+  // the rows' queries as A fragments: hi in rows 0-7, lo in rows 8-15
+  uint32_t ya[RT][NS][4];
+  int lim[RT], seen_by_all = it.k1;
+  {
+    const __nv_bfloat16* y = at<__nv_bfloat16>(q.a, q.p.o_y);
+    const int64_t lo = (int64_t)q.a.Hk * q.p.all * DP;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      const int row = rt * 8 + g;
+      const bool ok = row < it.nrows;
+      const __nv_bfloat16* src = y + ((int64_t)hk * q.p.all + it.row0 + (ok ? row : 0)) * DP + 2 * t;
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        ya[rt][s][0] = ok ? *reinterpret_cast<const uint32_t*>(src + 16 * s) : 0u;
+        ya[rt][s][1] = ok ? *reinterpret_cast<const uint32_t*>(src + lo + 16 * s) : 0u;
+        ya[rt][s][2] = ok ? *reinterpret_cast<const uint32_t*>(src + 16 * s + 8) : 0u;
+        ya[rt][s][3] = ok ? *reinterpret_cast<const uint32_t*>(src + lo + 16 * s + 8) : 0u;
+      }
+      lim[rt] = ok ? visible_keys(q, it, row) : 0;
+      if (ok) seen_by_all = min(seen_by_all, lim[rt]);
+    }
+    for (int o = 4; o < 32; o <<= 1)
+      seen_by_all = min(seen_by_all, __shfl_xor_sync(0xffffffffu, seen_by_all, o));
+  }
+  float o[RT][NT][4], l[RT], ref[RT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    l[rt] = 0.f;
+    ref[rt] = -INFINITY;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[rt][n][e] = 0.f;
+  }
+
+  const int lr = lane & 7, lg = lane >> 3;                // ldmatrix: row in, and number of, a matrix
+  for (int i = 0; i < mine; ++i) {
+    cp_wait<S - 2>();
+    __syncwarp();
+    {
+      const int64_t row = next;
+      next = lookup(i + S);
+      if (i + S - 1 < mine) issue(i + S - 1, row);
+      cp_commit();
+    }
+    const uint32_t k0 = ring0 + (uint32_t)(i % S) * 2 * C::kTile, v0 = k0 + C::kTile;
+    float s[RT][2][4];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[rt][n][e] = 0.f;
+#pragma unroll
+    for (int st = 0; st < NS; ++st) {
+      uint32_t b[4];
+      ldsm4(b, k0 + tile_off<DP>((lg >> 1) * 8 + lr, 2 * st + (lg & 1)));
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        mma16816(s[rt][0], ya[rt][st], b[0], b[1]);
+        mma16816(s[rt][1], ya[rt][st], b[2], b[3]);
+      }
+    }
+    const int key0 = it.k0 + (warp + i * kWarps) * kKeys + 2 * t;
+    uint32_t pa[RT][4];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      float v[4];                                         // keys key0 + {0, 1, 8, 9} of row g
+      const int end = it.k1 < lim[rt] ? it.k1 : lim[rt];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x = s[rt][e >> 1][e & 1] + s[rt][e >> 1][2 + (e & 1)];
+        v[e] = key0 + (e >> 1) * 8 + (e & 1) < end ? x : -INFINITY;
+      }
+      float top = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const bool move = top > ref[rt] + 8.f;              // (-inf + 8 = -inf: the first visible key)
+      if (__any_sync(0xffffffffu, move)) {
+        const float now = move ? top : ref[rt];
+        const float f = move ? exp2f(ref[rt] - now) : 1.f;
+        ref[rt] = now;
+        l[rt] *= f;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[rt][n][e] *= f;
+      }
+      const float r = ref[rt] == -INFINITY ? 0.f : ref[rt];
+      float hi[4], lo[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float p = tc::ex2(v[e] - r);
+        l[rt] += p;
+        hi[e] = __bfloat162float(__float2bfloat16_rn(p));
+        lo[e] = p - hi[e];
+      }
+      pa[rt][0] = tc::pack_bf16(hi[0], hi[1]);
+      pa[rt][1] = tc::pack_bf16(lo[0], lo[1]);
+      pa[rt][2] = tc::pack_bf16(hi[2], hi[3]);
+      pa[rt][3] = tc::pack_bf16(lo[2], lo[3]);
+    }
+    // A weight of 0 does not cancel an infinite or NaN value of a key that only other rows
+    // see (causal, the last T - 1 keys): a tile with one adds its values key by key.
+    const int tile0 = it.k0 + (warp + i * kWarps) * kKeys;
+    if (tile0 + kKeys > seen_by_all && tile_non_finite<DP>(v0, lane)) {
+#pragma unroll 1
+      for (int kk = 0; kk < kKeys; ++kk) {
+        const int src = (lane & ~3) | ((kk & 7) >> 1);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+          const uint32_t h2 = __shfl_sync(0xffffffffu, kk < 8 ? pa[rt][0] : pa[rt][2], src);
+          const uint32_t l2 = __shfl_sync(0xffffffffu, kk < 8 ? pa[rt][1] : pa[rt][3], src);
+          if (tile0 + kk >= min(it.k1, lim[rt])) continue;
+          const float p = bf16_half(h2, kk & 1) + bf16_half(l2, kk & 1);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const uint32_t w = ld_shared_u32(v0 + tile_off<DP>(kk, n) + 4 * t);
+            o[rt][n][0] = fmaf(p, bf16_half(w, 0), o[rt][n][0]);
+            o[rt][n][1] = fmaf(p, bf16_half(w, 1), o[rt][n][1]);
+          }
+        }
+      }
+      __syncwarp();
+      continue;
+    }
+#pragma unroll
+    for (int n = 0; n < NT; n += 2) {
+      uint32_t b[4];
+      ldsm4_t(b, v0 + tile_off<DP>((lg & 1) * 8 + lr, n + (lg >> 1)));
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        mma16816(o[rt][n], pa[rt], b[0], b[1]);
+        mma16816(o[rt][n + 1], pa[rt], b[2], b[3]);
+      }
+    }
+    __syncwarp();                                         // the slot may be filled again
+  }
+  cp_wait<0>();
+
+  // join the four warps: references and weights, then sums (in the rings' memory)
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    l[rt] += __shfl_xor_sync(0xffffffffu, l[rt], 1);
+    l[rt] += __shfl_xor_sync(0xffffffffu, l[rt], 2);
+  }
+  __syncthreads();
+  float* sml = reinterpret_cast<float*>(smem);            // [warp][RB][2]
+  float* sac = sml + kWarps * RB * 2;                     // [warp][RB][DP]
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    const int row = rt * 8 + g;
+    if (t == 0) {
+      sml[(warp * RB + row) * 2] = ref[rt];
+      sml[(warp * RB + row) * 2 + 1] = l[rt];
+    }
+    float* dst = sac + (warp * RB + row) * DP + 2 * t;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+      *reinterpret_cast<float2*>(dst + 8 * n) =
+          make_float2(o[rt][n][0] + o[rt][n][2], o[rt][n][1] + o[rt][n][3]);
+  }
+  __syncthreads();
+  for (int idx = tid; idx < it.nrows * (d / 4); idx += kWarps * 32) {
+    const int row = idx / (d / 4), c = (idx - row * (d / 4)) * 4;
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sml[(w * RB + row) * 2]);
+    const float r = top == -INFINITY ? 0.f : top;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    float lw = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = exp2f(sml[(w * RB + row) * 2] - r);
+      const float4 x = *reinterpret_cast<const float4*>(sac + (w * RB + row) * DP + c);
+      lw = fmaf(f, sml[(w * RB + row) * 2 + 1], lw);
+      a.x = fmaf(f, x.x, a.x); a.y = fmaf(f, x.y, a.y);
+      a.z = fmaf(f, x.z, a.z); a.w = fmaf(f, x.w, a.w);
+    }
+    *reinterpret_cast<float4*>(it.acc + (int64_t)row * d + c) = a;
+    if (c == 0) {
+      it.ml[2 * row] = top;
+      it.ml[2 * row + 1] = lw;
+    }
+  }
+}
+
+template <int DP, int RT>
+cudaError_t launch(const Params& q, long long n) {
+  using C = Cfg<DP>;
+  static int smem_set[64];
+  cudaError_t e = set_smem_limit_once((const void*)range_mma_kernel<DP, RT>, (int)C::kSmem, smem_set);
+  if (e != cudaSuccess) return e;
+  range_mma_kernel<DP, RT><<<dim3((unsigned)n, q.a.Hk), kWarps * 32, C::kSmem, q.a.stream>>>(q);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_ranges_mma(const Params& q) {
+  const int dp = q.p.dp, rb = mma_rows(dp, q.p.rows);
+  long long n = (long long)q.p.cap * ((q.p.rows + rb - 1) / rb);
+  if (q.a.prefix_len > 0) n += (long long)q.p.p_splits * ((q.p.all + rb - 1) / rb);
+  if (dp == 256) return launch<256, 1>(q, n);
+  if (dp == 128) return rb == 8 ? launch<128, 1>(q, n) : launch<128, 2>(q, n);
+  return rb == 8 ? launch<64, 1>(q, n) : launch<64, 2>(q, n);
+}
+
+}  // namespace cache
+}  // namespace dark

@@ -165,4 +165,56 @@ size_t omega_workspace_bytes(int heads, int m, int r, int orthogonal);
 cudaError_t launch_sample_omega(uint64_t seed, uint64_t draw, int heads, int m, int r,
                                 int orthogonal, float* omega, void* ws, cudaStream_t stream);
 
+// Rows of one tensor of a head-norm, rotation or cache-append call: `heads` heads of
+// every token, normed where gamma is given and rotated where `rotate` is set.
+struct RowSet {
+  const void *x, *g;              // rows; cotangents (backward)
+  void* y;                        // results: strided rows, or the cache's pages
+  int64_t xs[3], gs[3], ys[3];    // element strides {b, h, l}
+  const float* gamma;             // [gheads][d] or null
+  float* dgamma;                  // [gheads][d] (backward)
+  int heads, gheads, rotate;
+};
+struct NormRopeArgs {
+  RowSet set[2];                  // q and k, or k and v; set[1].heads may be 0
+  dark_rope rope;                 // dims = 0: no rotation
+  dark_dtype dtype;
+  float eps;
+  int B, L, d;
+  const int32_t* positions;       // [B][L], or null: pos0 + place in the sequence
+  int64_t pos0;
+  // append: rows go to place lens[b] + l of sequence b (lens null: not an append)
+  const int32_t *lens, *new_lens, *table;
+  int max_pages, pages, page;
+  float* part;                    // backward: the warps' partial dgamma rows
+  int* dev_status;
+  cudaStream_t stream;
+};
+cudaError_t launch_norm_rope(const NormRopeArgs& a);
+size_t norm_rope_bwd_workspace_bytes(int B, int H, int Hk, int L, int d);
+cudaError_t launch_norm_rope_bwd(const NormRopeArgs& a);
+
+// Exact-mode attention over a paged cache, with a prefix shared by all sequences.
+struct CacheAttnArgs {
+  int heads_w, m, r, d;
+  dark_dtype dtype;
+  const void* w;                  // projection buffer: the last r rows of a head are c_m M
+  const void *kp, *vp;            // pages [pages][Hk][page][d]
+  int pages, Hk, page;
+  const void* q;
+  void* out;
+  int64_t qs[3], os[3];           // element strides {b, h, t}
+  int B, H, T;
+  const int32_t* prefix_pages;
+  int prefix_len;
+  const int32_t *table, *lens;    // [B][max_pages], [B]
+  int max_pages;
+  int flags;
+  void* ws;
+  int* dev_status;
+  cudaStream_t stream;
+};
+size_t cache_attention_workspace_bytes(const CacheAttnArgs& a);
+cudaError_t launch_cache_attention(const CacheAttnArgs& a);
+
 }  // namespace dark

@@ -34,7 +34,10 @@ EXPORTS = ("dark_abi_version", "dark_status_string", "dark_projection_bytes",
            "dark_attention_bwd_workspace_bytes", "dark_attention_bwd",
            "dark_sample_omega_workspace_bytes", "dark_sample_omega", "dark_redraw_schedule_init",
            "dark_redraw_on_forward", "dark_redraw_request", "dark_redraw_set_fixed",
-           "dark_auto_uses_exact", "dark_set_test_stall_cycles")
+           "dark_auto_uses_exact", "dark_set_test_stall_cycles", "dark_rope_init",
+           "dark_qk_norm_rope_fwd", "dark_qk_norm_rope_bwd_workspace_bytes",
+           "dark_qk_norm_rope_bwd", "dark_kv_append", "dark_cache_attention_workspace_bytes",
+           "dark_cache_attention_fwd")
 
 
 class dark_projection(ctypes.Structure):
@@ -52,6 +55,17 @@ class dark_state(ctypes.Structure):
 class dark_redraw_schedule(ctypes.Structure):
     _fields_ = [("seed", ctypes.c_uint64), ("draw", ctypes.c_uint64),
                 ("interval", ctypes.c_int64), ("count", ctypes.c_int64), ("fixed", ctypes.c_int)]
+
+
+class dark_rope(ctypes.Structure):
+    _fields_ = [("dims", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("turns", ctypes.c_uint64 * 128)]
+
+
+class dark_kv_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("pages", ctypes.c_int),
+                ("heads", ctypes.c_int), ("page_size", ctypes.c_int), ("d", ctypes.c_int),
+                ("dtype", ctypes.c_int)]
 
 
 _P = ctypes.POINTER
@@ -114,6 +128,32 @@ _lib.dark_attention_bwd.argtypes = [_vp, _i, _vp, _i, _i, _i, _i, _i, _vp, _vp, 
                                     _P(ctypes.c_int64), _vp, _P(ctypes.c_int64), _i, _i, _i, _vp,
                                     _i, _vp, _vp, _vp, _P(ctypes.c_int64), _vp, _vp, _sz, _vp,
                                     _vp]
+
+_s3 = _P(ctypes.c_int64)
+_lib.dark_rope_init.restype = _i
+_lib.dark_rope_init.argtypes = [_P(dark_rope), _i, ctypes.c_double, ctypes.c_double, _i]
+_lib.dark_qk_norm_rope_fwd.restype = _i
+_lib.dark_qk_norm_rope_fwd.argtypes = [_vp, _s3, _vp, _s3, _vp, _s3, _vp, _s3, _vp, _i, _vp, _i,
+                                       ctypes.c_float, _P(dark_rope), _vp, ctypes.c_int64, _i, _i,
+                                       _i, _i, _i, _i, _vp, _vp]
+_lib.dark_qk_norm_rope_bwd_workspace_bytes.restype = _sz
+_lib.dark_qk_norm_rope_bwd_workspace_bytes.argtypes = [_i] * 5
+_lib.dark_qk_norm_rope_bwd.restype = _i
+_lib.dark_qk_norm_rope_bwd.argtypes = [_vp, _s3, _vp, _s3, _vp, _s3, _vp, _s3, _vp, _s3, _vp, _s3,
+                                       _vp, _i, _vp, _i, _vp, _vp, ctypes.c_float, _P(dark_rope),
+                                       _vp, ctypes.c_int64, _i, _i, _i, _i, _i, _i, _vp, _sz, _vp,
+                                       _vp]
+_lib.dark_kv_append.restype = _i
+_lib.dark_kv_append.argtypes = [_P(dark_kv_cache), _vp, _s3, _vp, _s3, _i, _i, _vp, _i, _vp, _vp,
+                                _vp, _i, ctypes.c_float, _P(dark_rope), _vp, ctypes.c_int64, _vp,
+                                _vp]
+_lib.dark_cache_attention_workspace_bytes.restype = _sz
+_lib.dark_cache_attention_workspace_bytes.argtypes = [_P(dark_projection), _P(dark_kv_cache)] + \
+    [_i] * 5
+_lib.dark_cache_attention_fwd.restype = _i
+_lib.dark_cache_attention_fwd.argtypes = [_P(dark_projection), _P(dark_kv_cache), _vp, _s3, _vp,
+                                          _s3, _i, _i, _i, _vp, _i, _vp, _i, _vp, _i, _vp, _sz,
+                                          _vp, _vp]
 
 
 class DarkError(RuntimeError):
@@ -355,6 +395,246 @@ def dark_sample_omega(seed: int, draw: int, omega, orthogonal: bool = True, ws=N
     _check(_lib.dark_sample_omega(seed, draw, heads, m, r, int(orthogonal), _ptr(omega), _ptr(ws),
                                   0 if ws is None else ws.numel() * ws.element_size(),
                                   _stream(stream)))
+
+
+# ---- head norms with rotation, paged cache, exact mode over it --------------
+# These calls take their sizes from the tensors, so the binding checks that the
+# tensors agree; what the C ABI checks (ranges, alignment, flags) stays there.
+
+_DTYPES = {torch.float32: DARK_F32, torch.bfloat16: DARK_BF16}
+_INT32, _F32 = (torch.int32,), (torch.float32,)
+
+
+def _want(t, name, shape, dtypes, dev):
+    """A dense tensor of the given shape, type and device."""
+    if t.shape != shape or t.dtype not in dtypes or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor of shape {tuple(shape)}, type "
+                         f"{' or '.join(str(x) for x in dtypes)} on {dev}")
+    return t.data_ptr()
+
+
+def _rows(t, name, B, L, d, dtype, dev):
+    """A [B][heads][L][d] tensor with a unit d stride: pointer, strides, heads."""
+    s = t.stride()
+    if t.dim() != 4 or t.shape[0] != B or t.shape[2] != L or t.shape[3] != d:
+        raise ValueError(f"{name}: expected [B][heads][L][d] = [{B}][..][{L}][{d}]")
+    if s[3] != 1 or t.dtype != dtype or t.device != dev:
+        raise ValueError(f"{name}: expected type {dtype} and a unit d stride, on {dev}")
+    return t.data_ptr(), _S3(s[0], s[1], s[2]), t.shape[1]
+
+
+_S3 = ctypes.c_int64 * 3
+
+
+def _weight(g, name, heads, d, dev):
+    """A norm weight [1 or heads][d] (or [d]): pointer, rows; None: (None, 1)."""
+    if g is None:
+        return None, 1
+    n = 1 if g.dim() == 1 else g.shape[0]
+    if g.dim() > 2 or g.shape[-1] != d or n not in (1, heads) or g.dtype != torch.float32 \
+            or g.device != dev or not g.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous fp32 tensor [1 or {heads}][{d}] on {dev}")
+    return g.data_ptr(), n
+
+
+def _first(t, name):
+    """Sizes of the tensor that the others are held against."""
+    if t.dim() != 4 or t.dtype not in _DTYPES:
+        raise ValueError(f"{name}: expected a [B][heads][L][d] tensor of fp32 or bf16")
+    return t.shape[0], t.shape[2], t.shape[3]
+
+
+class _on:
+    """Makes a tensor's device the current one for a call, where it is another."""
+
+    def __init__(self, dev):
+        self.c = None
+        if dev.type == "cuda" and dev.index != torch.cuda.current_device():
+            self.c = torch.cuda.device(dev)
+
+    def __enter__(self):
+        if self.c is not None:
+            self.c.__enter__()
+
+    def __exit__(self, *e):
+        if self.c is not None:
+            self.c.__exit__(*e)
+
+
+def dark_rope_init(dims: int, base: float = 10000.0, scale: float = 1.0,
+                   interleaved: bool = False) -> dark_rope:
+    """The rotation handle of the calls below (host memory; no device work)."""
+    r = dark_rope()
+    _check(_lib.dark_rope_init(ctypes.byref(r), dims, base, scale, int(interleaved)))
+    return r
+
+
+def dark_qk_norm_rope_fwd(q, k, q_out, k_out, gamma_q=None, gamma_k=None, eps: float = 1e-6,
+                          rope: dark_rope | None = None, positions=None, pos0: int = 0,
+                          dev_status=None, stream=None) -> None:
+    """Norms the head rows of q [B][H][L][d] and k [B][Hk][L][d] (k and k_out may be None)
+    and rotates them by their positions (int32 [B][L], or None: pos0 + l)."""
+    B, L, d = _first(q, "q")
+    dt, dev = q.dtype, q.device
+    qp, qs, H = _rows(q, "q", B, L, d, dt, dev)
+    op, os_, n = _rows(q_out, "q_out", B, L, d, dt, dev)
+    if (k is None) != (k_out is None):
+        raise ValueError("k and k_out: both or neither")
+    kp = ks = kop = kos = None
+    Hk = 0
+    if k is not None:
+        kp, ks, Hk = _rows(k, "k", B, L, d, dt, dev)
+        kop, kos, nk = _rows(k_out, "k_out", B, L, d, dt, dev)
+    if n != H or (k is not None and nk != Hk):
+        raise ValueError("results have other head counts than their inputs")
+    gq, hq = _weight(gamma_q, "gamma_q", H, d, dev)
+    gk, hk = _weight(gamma_k, "gamma_k", Hk, d, dev)
+    pp = None if positions is None else _want(positions, "positions", (B, L), _INT32, dev)
+    with _on(dev):
+        _check(_lib.dark_qk_norm_rope_fwd(qp, qs, kp, ks, op, os_, kop, kos, gq, hq, gk, hk, eps,
+                                          rope, pp, pos0, B, H, Hk, L, d, _DTYPES[dt],
+                                          _ptr(dev_status), _stream(stream)))
+
+
+def dark_qk_norm_rope_bwd_workspace_bytes(B: int, H: int, Hk: int, L: int, d: int) -> int:
+    return _lib.dark_qk_norm_rope_bwd_workspace_bytes(B, H, Hk, L, d)
+
+
+def alloc_qk_norm_rope_bwd_workspace(B: int, H: int, Hk: int, L: int, d: int, device):
+    """A workspace of the size dark_qk_norm_rope_bwd_workspace_bytes asks for."""
+    n = dark_qk_norm_rope_bwd_workspace_bytes(B, H, Hk, L, d)
+    return torch.empty(max(n, WS_HEADER_BYTES), dtype=torch.uint8, device=device)
+
+
+def dark_qk_norm_rope_bwd(q, k, dq_out, dk_out, dq, dk, gamma_q=None, gamma_k=None,
+                          dgamma_q=None, dgamma_k=None, eps: float = 1e-6,
+                          rope: dark_rope | None = None, positions=None, pos0: int = 0, ws=None,
+                          dev_status=None, stream=None) -> None:
+    """Gradients of dark_qk_norm_rope_fwd: dq, dk of the inputs' type and dgamma_q,
+    dgamma_k (fp32, of the weights' shape). ws: see alloc_qk_norm_rope_bwd_workspace."""
+    B, L, d = _first(q, "q")
+    dt, dev = q.dtype, q.device
+    qp, qs, H = _rows(q, "q", B, L, d, dt, dev)
+    gp, gs, n1 = _rows(dq_out, "dq_out", B, L, d, dt, dev)
+    op, os_, n2 = _rows(dq, "dq", B, L, d, dt, dev)
+    if not (k is None) == (dk_out is None) == (dk is None):
+        raise ValueError("k, dk_out and dk: all or none")
+    kp = ks = kgp = kgs = kop = kos = None
+    Hk = n3 = n4 = 0
+    if k is not None:
+        kp, ks, Hk = _rows(k, "k", B, L, d, dt, dev)
+        kgp, kgs, n3 = _rows(dk_out, "dk_out", B, L, d, dt, dev)
+        kop, kos, n4 = _rows(dk, "dk", B, L, d, dt, dev)
+    if (n1, n2, n3, n4) != (H, H, Hk, Hk):
+        raise ValueError("gradients have other head counts than their inputs")
+    gq, hq = _weight(gamma_q, "gamma_q", H, d, dev)
+    gk, hk = _weight(gamma_k, "gamma_k", Hk, d, dev)
+    dgq, hdq = _weight(dgamma_q, "dgamma_q", H, d, dev)
+    dgk, hdk = _weight(dgamma_k, "dgamma_k", Hk, d, dev)
+    if (gq is not None and dgq is not None and hdq != hq) or \
+            (gk is not None and dgk is not None and hdk != hk):
+        raise ValueError("a weight's gradient has the weight's shape")
+    pp = None if positions is None else _want(positions, "positions", (B, L), _INT32, dev)
+    with _on(dev):
+        _check(_lib.dark_qk_norm_rope_bwd(qp, qs, kp, ks, gp, gs, kgp, kgs, op, os_, kop, kos, gq,
+                                          hq, gk, hk, dgq, dgk, eps, rope, pp, pos0, B, H, Hk, L,
+                                          d, _DTYPES[dt], *_ws(ws, dev), _ptr(dev_status),
+                                          _stream(stream)))
+
+
+def _ws(ws, dev):
+    """Pointer and bytes of a workspace tensor."""
+    if ws is None:
+        return None, 0
+    if ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"ws: expected a contiguous tensor on {dev}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def kv_cache(k_pages, v_pages) -> dark_kv_cache:
+    """The handle of a paged cache: tensors [pages][heads][page_size][d] of keys and values,
+    which have to live as long as it does."""
+    if k_pages.dim() != 4 or k_pages.dtype not in _DTYPES:
+        raise ValueError("k_pages: expected a [pages][heads][page_size][d] tensor of fp32 or bf16")
+    _want(k_pages, "k_pages", k_pages.shape, (k_pages.dtype,), k_pages.device)
+    _want(v_pages, "v_pages", k_pages.shape, (k_pages.dtype,), k_pages.device)
+    c = dark_kv_cache(k_pages.data_ptr(), v_pages.data_ptr(), *k_pages.shape,
+                      _DTYPES[k_pages.dtype])
+    c.tensors = (k_pages, v_pages)
+    return c
+
+
+def _cache_dtype(cache, t, name):
+    if t.dtype not in _DTYPES or _DTYPES[t.dtype] != cache.dtype:
+        raise ValueError(f"{name}: expected the cache's type")
+
+
+def _lists(page_table, lens, B, dev):
+    """A page table [B][max_pages] and lengths [B], int32: pointers and max_pages."""
+    if page_table.dim() != 2:
+        raise ValueError("page_table: expected int32 [B][max_pages]")
+    n = page_table.shape[1]
+    return (_want(page_table, "page_table", (B, n), _INT32, dev), n,
+            _want(lens, "lens", (B,), _INT32, dev))
+
+
+def dark_kv_append(cache: dark_kv_cache, k, v, page_table, lens, new_lens=None, gamma_k=None,
+                   eps: float = 1e-6, rope: dark_rope | None = None, positions=None,
+                   pos0: int = 0, dev_status=None, stream=None) -> None:
+    """Appends k, v [B][heads][T][d] behind the lens[b] tokens of every sequence, the keys
+    normed and rotated on the way. page_table int32 [B][max_pages], lens int32 [B], new_lens
+    int32 [B] (None: all T), positions int32 [B][T] (None: pos0 + lens[b] + t)."""
+    B, T, d = _first(k, "k")
+    dt, dev = k.dtype, k.device
+    _cache_dtype(cache, k, "k")
+    kp, ks, n1 = _rows(k, "k", B, T, d, dt, dev)
+    vp, vs, n2 = _rows(v, "v", B, T, d, dt, dev)
+    if n1 != cache.heads or n2 != cache.heads or d != cache.d:
+        raise ValueError("k, v: expected the cache's heads and d")
+    tp, max_pages, lp = _lists(page_table, lens, B, dev)
+    np_ = None if new_lens is None else _want(new_lens, "new_lens", (B,), _INT32, dev)
+    pp = None if positions is None else _want(positions, "positions", (B, T), _INT32, dev)
+    g, hg = _weight(gamma_k, "gamma_k", n1, d, dev)
+    with _on(dev):
+        _check(_lib.dark_kv_append(cache, kp, ks, vp, vs, B, T, tp, max_pages, lp, np_, g, hg, eps,
+                                   rope, pp, pos0, _ptr(dev_status), _stream(stream)))
+
+
+def dark_cache_attention_workspace_bytes(proj: dark_projection, cache: dark_kv_cache, B: int,
+                                         H: int, T: int, prefix_len: int, max_pages: int) -> int:
+    return _lib.dark_cache_attention_workspace_bytes(proj, cache, B, H, T, prefix_len, max_pages)
+
+
+def alloc_cache_attention_workspace(proj: dark_projection, cache: dark_kv_cache, B: int, H: int,
+                                    T: int, prefix_len: int, max_pages: int, device):
+    """A workspace of the size dark_cache_attention_workspace_bytes asks for."""
+    n = dark_cache_attention_workspace_bytes(proj, cache, B, H, T, prefix_len, max_pages)
+    return torch.empty(max(n, WS_HEADER_BYTES), dtype=torch.uint8, device=device)
+
+
+def dark_cache_attention_fwd(proj: dark_projection, cache: dark_kv_cache, q, out, page_table, lens,
+                             prefix_pages=None, prefix_len: int = 0, flags: int = 0, ws=None,
+                             dev_status=None, stream=None) -> None:
+    """Exact-mode attention of q [B][H][T][d] over the shared prefix (prefix_pages int32
+    [ceil(prefix_len / page_size)]) and each sequence's lens[b] own tokens. ws: see
+    alloc_cache_attention_workspace."""
+    B, T, d = _first(q, "q")
+    dt, dev = q.dtype, q.device
+    _cache_dtype(cache, q, "q")
+    qp, qs, H = _rows(q, "q", B, T, d, dt, dev)
+    op, os_, n = _rows(out, "out", B, T, d, dt, dev)
+    if n != H or d != cache.d:
+        raise ValueError("q, out: expected equal head counts and the cache's d")
+    tp, max_pages, lp = _lists(page_table, lens, B, dev)
+    xp = None
+    if prefix_len > 0 and prefix_pages is not None:
+        if prefix_pages.dim() != 1 or prefix_pages.shape[0] * cache.page_size < prefix_len:
+            raise ValueError("prefix_pages: expected int32 [ceil(prefix_len / page_size)]")
+        xp = _want(prefix_pages, "prefix_pages", prefix_pages.shape, _INT32, dev)
+    with _on(dev):
+        _check(_lib.dark_cache_attention_fwd(proj, cache, qp, qs, op, os_, B, H, T, xp, prefix_len,
+                                             tp, max_pages, lp, flags, *_ws(ws, dev),
+                                             _ptr(dev_status), _stream(stream)))
 
 
 class RedrawSchedule:
