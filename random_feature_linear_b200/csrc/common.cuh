@@ -36,6 +36,13 @@ __device__ __forceinline__ void report(int* dev_status, int code) {
   if (dev_status != nullptr) atomicCAS(dev_status, 0, code);
 }
 
+// Launches in a row whose later ones start while the earlier ones end (launch_dependent):
+// the earlier kernel lets the next one start with pdl_launch, which touches nothing of the
+// earlier one's results before pdl_wait (then that kernel has ended and its writes are
+// seen). Without such a launch both do nothing.
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);

@@ -165,6 +165,24 @@ size_t omega_workspace_bytes(int heads, int m, int r, int orthogonal);
 cudaError_t launch_sample_omega(uint64_t seed, uint64_t draw, int heads, int m, int r,
                                 int orthogonal, float* omega, void* ws, cudaStream_t stream);
 
+// Launches `kernel` so that it may start while the stream's last kernel ends; the kernel
+// waits for it with pdl_wait before it touches that kernel's results.
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem,
+                             cudaStream_t stream, const A&... args) {
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c = {};
+  c.gridDim = grid;
+  c.blockDim = block;
+  c.dynamicSmemBytes = smem;
+  c.stream = stream;
+  c.attrs = at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, args...);
+}
+
 // Rows of one tensor of a head-norm, rotation or cache-append call: `heads` heads of
 // every token, normed where gamma is given and rotated where `rotate` is set.
 struct RowSet {

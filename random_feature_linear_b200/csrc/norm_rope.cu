@@ -12,11 +12,9 @@
 // 64-bit position (an fp32 product would be off by a radian at p ~ 1e7); its upper
 // 32 bits give an fp32 angle, off by at most 2^-25 turns of pi.
 //
-// Every kernel is bound by reading and writing its rows (2, 3 or 4 accesses of
-// n elements and ~20 instructions an element). A lane group of 1-32 lanes holds a
-// row in registers, eight elements a lane: one read, one shuffle reduction, one
-// write. A CTA takes a tile of tokens and all heads of a group, so that a token's
-// cosines and sines are computed once, in shared memory, for its heads.
+// Every kernel is bound by reading and writing its rows (2, 3 or 4 accesses of n
+// elements). A lane group of 1-32 lanes holds a row in registers: one read, one shuffle
+// reduction, one write.
 #include <math.h>
 
 #include "common.cuh"
@@ -25,454 +23,689 @@
 namespace dark {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kTile = 32;                 // tokens of a CTA's tile, at most
+constexpr int kThreads = 256, kWarps = kThreads / 32;   // of the backward pass
+constexpr int kRowWarps = 4;                            // of the forward pass
 
-// N elements of T as raw words, loaded and stored at once (N sizeof(T) in 2..16).
-template <int kBytes> struct Raw;
-template <> struct Raw<2> { using type = uint16_t; };
-template <> struct Raw<4> { using type = uint32_t; };
-template <> struct Raw<8> { using type = uint2; };
-template <> struct Raw<16> { using type = uint4; };
-template <typename T, int N>
-union Pack {
-  typename Raw<(int)sizeof(T) * N>::type raw;
-  T v[N];
-  __device__ Pack() {}
+// Two fp32 values in one 64-bit register; an operation is one instruction for both (each
+// rounded as the scalar one is).
+struct F2 {
+  uint64_t v;
+  __device__ __forceinline__ F2() {}
+  __device__ __forceinline__ F2(float x, float y) {
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+  }
+  __device__ __forceinline__ explicit F2(float x) : F2(x, x) {}
+  __device__ __forceinline__ float2 get() const {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+  }
+  __device__ __forceinline__ float sum() const {
+    const float2 r = get();
+    return r.x + r.y;
+  }
 };
-template <typename T, int N>
-__device__ __forceinline__ void load(Pack<T, N>& p, const T* src) {
-  p.raw = *reinterpret_cast<const decltype(p.raw)*>(src);
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
 }
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+
+// A run of N elements of T as raw words, loaded and stored at once (2 to 16 bytes).
 template <typename T, int N>
-__device__ __forceinline__ void store(T* dst, const Pack<T, N>& p) {
-  *reinterpret_cast<decltype(p.raw)*>(dst) = p.raw;
+struct Run {
+  static constexpr int kBytes = (int)sizeof(T) * N, kWords = kBytes < 4 ? 1 : kBytes / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const T* src) {
+    if constexpr (kBytes == 16) {
+      const uint4 x = *reinterpret_cast<const uint4*>(src);
+      w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+    } else if constexpr (kBytes == 8) {
+      const uint2 x = *reinterpret_cast<const uint2*>(src);
+      w[0] = x.x; w[1] = x.y;
+    } else if constexpr (kBytes == 4) {
+      w[0] = *reinterpret_cast<const uint32_t*>(src);
+    } else {
+      w[0] = *reinterpret_cast<const uint16_t*>(src);
+    }
+  }
+  __device__ __forceinline__ void store(T* dst) const {
+    if constexpr (kBytes == 16) *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+    else if constexpr (kBytes == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+    else if constexpr (kBytes == 4) *reinterpret_cast<uint32_t*>(dst) = w[0];
+    else *reinterpret_cast<uint16_t*>(dst) = (uint16_t)w[0];
+  }
+};
+
+// A lane's own slot of shared memory: filled by an asynchronous copy (2-byte runs by a
+// plain one), read back by the same lane once the copies' group has arrived.
+template <typename T, int N>
+__device__ __forceinline__ void fetch(uint32_t slot, const T* src, bool ok) {       // zeros if not
+  constexpr int kBytes = Run<T, N>::kBytes;
+  if constexpr (kBytes == 16) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(slot), "l"(src), "r"(ok ? 16 : 0)
+                 : "memory");
+  } else if constexpr (kBytes >= 4) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(slot), "l"(src), "n"(kBytes),
+                 "r"(ok ? kBytes : 0)
+                 : "memory");
+  } else {
+    const uint16_t v = ok ? *reinterpret_cast<const uint16_t*>(src) : (uint16_t)0;
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(slot), "h"(v) : "memory");
+  }
+}
+__device__ __forceinline__ void fetch_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void fetch_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+
+// The 2 N values of a unit as N pairs: N / 2 neighbours from each run, or one value of
+// each run for N = 1.
+template <typename T, int N>
+__device__ __forceinline__ void widen(F2 (&v)[N], const Run<T, N>& lo, const Run<T, N>& hi) {
+  constexpr bool bf = sizeof(T) == 2;
+  auto low = [](uint32_t w) { return __uint_as_float(bf ? w << 16 : w); };
+  if constexpr (N == 1) {
+    v[0] = F2(low(lo.w[0]), low(hi.w[0]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      if constexpr (bf) {
+        v[i] = F2(low(lo.w[i]), __uint_as_float(lo.w[i] & 0xffff0000u));
+        v[N / 2 + i] = F2(low(hi.w[i]), __uint_as_float(hi.w[i] & 0xffff0000u));
+      } else {
+        v[i] = F2(low(lo.w[2 * i]), low(lo.w[2 * i + 1]));
+        v[N / 2 + i] = F2(low(hi.w[2 * i]), low(hi.w[2 * i + 1]));
+      }
+    }
+  }
+}
+
+// What narrow() has seen of its results: 0 while all are finite, NaN from the first that
+// is not.
+struct Seen {
+  uint32_t h = 0;                         // two bf16
+  F2 f = F2(0.f);
+  __device__ __forceinline__ void add(float x) { f = fma2(F2(x, 0.f), F2(0.f), f); }
+  __device__ __forceinline__ void add(F2 x) { f = fma2(x, F2(0.f), f); }
+  __device__ __forceinline__ void add(uint32_t bf16x2) {
+    asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(h) : "r"(bf16x2), "r"(0u));
+  }
+  __device__ __forceinline__ bool bad() const {
+    return !(f.sum() == 0.f) || (h & 0x7fff7fffu) != 0;
+  }
+};
+
+// Rounds a unit's values to T.
+template <typename T, int N>
+__device__ __forceinline__ void narrow(Run<T, N>& lo, Run<T, N>& hi, const F2 (&v)[N], Seen& seen) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float2 x = v[i].get();
+      seen.add(v[i]);
+      if constexpr (N == 1) {
+        lo.w[0] = __float_as_uint(x.x);
+        hi.w[0] = __float_as_uint(x.y);
+      } else {
+        Run<T, N>& r = i < N / 2 ? lo : hi;
+        r.w[i % (N / 2) * 2] = __float_as_uint(x.x);
+        r.w[i % (N / 2) * 2 + 1] = __float_as_uint(x.y);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float2 x = v[i].get();
+      uint32_t w;
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(x.y), "f"(x.x));
+      seen.add(w);
+      if constexpr (N == 1) {
+        lo.w[0] = w & 0xffffu;
+        hi.w[0] = w >> 16;
+      } else {
+        (i < N / 2 ? lo : hi).w[i % (N / 2)] = w;
+      }
+    }
+  }
+}
+
+// A unit's weights (fp32; 16-byte aligned runs where N is 4 or 8).
+template <int N>
+__device__ __forceinline__ void load_weights(F2 (&w)[N], const float* lo, const float* hi) {
+  if constexpr (N >= 4) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const float4 a = __ldg(reinterpret_cast<const float4*>(lo) + i);
+      const float4 b = __ldg(reinterpret_cast<const float4*>(hi) + i);
+      w[2 * i] = F2(a.x, a.y);
+      w[2 * i + 1] = F2(a.z, a.w);
+      w[N / 2 + 2 * i] = F2(b.x, b.y);
+      w[N / 2 + 2 * i + 1] = F2(b.z, b.w);
+    }
+  } else if constexpr (N == 2) {
+    w[0] = F2(__ldg(lo), __ldg(lo + 1));
+    w[1] = F2(__ldg(hi), __ldg(hi + 1));
+  } else {
+    w[0] = F2(__ldg(lo), __ldg(hi));
+  }
 }
 
 // A lane's unit u of a row: N pairs (2 N elements) in two runs of N. Rotated units
 // take the pairs [N u, N u + N); the units behind them 2 N elements in a row.
-template <int N>
+template <int N, bool INTER>
 struct Unit {
-  int lo, hi, pair;                       // element offsets; first pair, -1: not rotated
-  __device__ Unit(int u, int rot, int inter) {
-    const int ru = rot / (2 * N);
-    if (u < ru) {
-      pair = N * u;
-      lo = inter ? 2 * N * u : N * u;
-      hi = inter ? lo + N : rot / 2 + N * u;
-    } else {
-      pair = -1;
-      lo = 2 * N * u;                     // = rot + 2 N (u - ru)
-      hi = lo + N;
+  int lo, hi;                             // element offsets of the two runs
+  bool turned;
+  __device__ Unit(int u, int rot) {
+    turned = u < rot / (2 * N);
+    const bool split = turned && !INTER;
+    lo = split ? N * u : 2 * N * u;
+    hi = split ? rot / 2 + N * u : lo + N;
+  }
+};
+
+// Cosines and sines of a unit's N pairs. turn rotates the unit's values by them.
+template <int N>
+struct Angles {
+  float c[N], s[N];
+};
+template <int N, bool INTER>
+__device__ __forceinline__ void turn(F2 (&v)[N], const Angles<N>& t) {
+  if constexpr (INTER || N == 1) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float2 x = v[i].get();
+      v[i] = F2(fmaf(x.x, t.c[i], -x.y * t.s[i]), fmaf(x.x, t.s[i], x.y * t.c[i]));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      // (a, b) -> (a c - b s, b c + a s), the minus in one of the products' operands
+      const F2 a = v[i], b = v[N / 2 + i], c(t.c[2 * i], t.c[2 * i + 1]), s(t.s[2 * i], t.s[2 * i + 1]);
+      v[i] = fma2(mul2(b, s), F2(-1.f), mul2(a, c));
+      v[N / 2 + i] = fma2(b, c, mul2(a, s));
     }
   }
-};
+}
 
-// Rotates a unit's 2 N values in place; `s` is +1, or -1 for the transpose.
-template <int N>
-__device__ __forceinline__ void turn(float (&x)[2 * N], const float2* cs, int inter, float s) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const float c = cs[i].x, t = s * cs[i].y;
-    float& a = inter ? x[2 * i] : x[i];
-    float& b = inter ? x[2 * i + 1] : x[N + i];
-    const float a0 = a, b0 = b;
-    a = fmaf(a0, c, -b0 * t);
-    b = fmaf(a0, t, b0 * c);
+__device__ __forceinline__ void angle(int64_t pos, uint64_t turns, float* c, float* s) {
+  const uint64_t phase = (uint64_t)pos * turns;
+  // [-2^31, 2^31) / 2^31 half turns
+  sincospif((float)(int32_t)(phase >> 32) * 4.656612873077393e-10f, s, c);
+}
+
+// Forward and append. A warp takes 32 / lanes tokens and the heads [h0, h0 + hchunk) of
+// both sets: a token's cosines and sines are computed once, into registers, and used for
+// all its heads, whose rows stream through S slots of shared memory a lane. N pairs a unit,
+// NU units a lane.
+template <typename T, int N, int NU, int S, bool INTER, bool APPEND>
+__global__ void __launch_bounds__(32 * kRowWarps) rows_kernel(const __grid_constant__ NormRopeArgs a,
+                                                              int lanes, int hchunk) {
+  using R = Run<T, N>;
+  __shared__ __align__(16) uint8_t ring[kRowWarps][S][NU][2][32 * R::kBytes];
+  __shared__ uint64_t turns[128];          // (lanes that index the parameters take turns)
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane / lanes, lu = lane % lanes, rows = 32 / lanes;
+  const uint32_t ntok = (uint32_t)a.B * a.L;
+  const uint32_t n0 = (blockIdx.x * kRowWarps + warp) * rows, n = n0 + g;
+  for (int i = threadIdx.x; i < a.rope.dims / 2; i += 32 * kRowWarps) turns[i] = a.rope.turns[i];
+  __syncthreads();
+  if (n0 >= ntok) return;
+  bool live = n < ntok;
+  const int b = live ? n / a.L : 0, l = live ? n - (uint32_t)b * a.L : 0;
+  int64_t place = l, row = 0;              // row: of head 0 in the cache
+  if constexpr (APPEND) {
+    live = live && (a.new_lens == nullptr || l < a.new_lens[b]);
+    const int have = live ? a.lens[b] : 0;
+    place += have;
+    if (live) {
+      const int64_t pg = place / a.page;
+      const int id = have >= 0 && pg < a.max_pages ? a.table[(int64_t)b * a.max_pages + pg] : -1;
+      live = id >= 0 && id < a.pages;
+      if (!live) report(a.dev_status, DARK_ERR_INVALID_ARG);
+      row = (int64_t)id * a.set[0].heads * a.page + place % a.page;
+    }
   }
-}
-
-__device__ __forceinline__ float group_sum(float v, int lanes) {
-  for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
-// What the kernels know of a tile's tokens, in shared memory.
-struct Token {
-  int b, l;
-  int64_t row;                            // append: cache row of head 0, or -1: not written
-};
-
-struct Tile {
-  uint64_t turns[128];
-  Token tok[kTile];
-  int64_t pos[kTile];
-};
-
-// Tokens [n0, n0 + count) of the call: their places, positions, and cosines and
-// sines (cs[token][pair], computed once for all heads of the CTA).
-__device__ __forceinline__ void fill_tile(const NormRopeArgs& a, Tile& t, float2* cs, int64_t n0,
-                                          int count) {
-  const int np = a.rope.dims / 2, tid = threadIdx.x;
-  for (int i = tid; i < np; i += kThreads) t.turns[i] = a.rope.turns[i];
-  if (tid < count) {
-    const int64_t n = n0 + tid;
-    Token k;
-    k.b = (int)(n / a.L);
-    k.l = (int)(n - (int64_t)k.b * a.L);
-    k.row = -1;
-    int64_t place = k.l;
-    if (a.lens != nullptr) {
-      const int have = a.lens[k.b];
-      place += have;
-      const bool fresh = a.new_lens == nullptr || k.l < a.new_lens[k.b];
-      if (fresh) {
-        const int64_t pg = place / a.page;
-        const int id = have >= 0 && pg < a.max_pages ? a.table[(int64_t)k.b * a.max_pages + pg] : -1;
-        if (id >= 0 && id < a.pages)
-          k.row = (int64_t)id * a.set[0].heads * a.page + place % a.page;
-        else
-          report(a.dev_status, DARK_ERR_INVALID_ARG);
+  // producer: the next head to fetch, its row, and where the second set's rows begin
+  const int heads0 = a.set[0].heads, first = (int)blockIdx.y * hchunk;
+  const int last = min(first + hchunk, heads0 + a.set[1].heads);
+  auto x_of = [&](int w, int h) {
+    return (const T*)a.set[w].x + b * a.set[w].xs[0] + l * a.set[w].xs[2] + h * a.set[w].xs[1];
+  };
+  auto y_of = [&](int w, int h) {
+    return APPEND ? (T*)a.set[w].y + (row + (int64_t)h * a.page) * a.d
+                  : (T*)a.set[w].y + b * a.set[w].ys[0] + l * a.set[w].ys[2] + h * a.set[w].ys[1];
+  };
+  int w = first >= heads0 ? 1 : 0;
+  int next = first;
+  const T* x = x_of(w, first - (w ? heads0 : 0));
+  int64_t xh = a.set[w].xs[1];
+  bool has[NU];
+  int lo_at[NU], hi_at[NU];
+#pragma unroll
+  for (int e = 0; e < NU; ++e) {
+    const Unit<N, INTER> un(lu + e * lanes, a.rope.dims);
+    has[e] = live && 2 * N * (lu + e * lanes) < a.d;
+    lo_at[e] = un.lo;
+    hi_at[e] = un.hi;
+  }
+  const uint32_t slots = (uint32_t)__cvta_generic_to_shared(&ring[warp][0][0][0][lane * R::kBytes]);
+  constexpr uint32_t kRun = 32 * R::kBytes, kStage = NU * 2 * kRun;
+  auto issue = [&](uint32_t slot) {
+    if (next < last) {
+#pragma unroll
+      for (int e = 0; e < NU; ++e) {
+        fetch<T, N>(slot + 2 * e * kRun, x + lo_at[e], has[e]);
+        fetch<T, N>(slot + (2 * e + 1) * kRun, x + hi_at[e], has[e]);
+      }
+      x += xh;
+      if (++next == heads0) {
+        x = x_of(1, 0);
+        xh = a.set[1].xs[1];
       }
     }
-    t.tok[tid] = k;
-    t.pos[tid] = a.positions != nullptr ? (int64_t)a.positions[n] : a.pos0 + place;
-  }
-  __syncthreads();
-  for (int i = tid; i < count * np; i += kThreads) {
-    const int k = i / np, p = i - k * np;
-    const uint64_t phase = (uint64_t)t.pos[k] * t.turns[p];
-    // [-2^31, 2^31) / 2^31 half turns
-    const float x = (float)(int32_t)(phase >> 32) * 4.656612873077393e-10f;
-    float s, c;
-    sincospif(x, &s, &c);
-    cs[i] = make_float2(c, s);
-  }
-  __syncthreads();
-}
-
-// Forward: U rows of one head in flight for every lane group. N pairs a unit, NU
-// units a lane. Rows are normed where the set has a gamma, turned where `rotate`.
-template <typename T, int N, int NU, int U>
-__global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ NormRopeArgs a,
-                                                        int lanes, int tile, int hchunk) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  Tile& t = *reinterpret_cast<Tile*>(smem);
-  float2* cs = reinterpret_cast<float2*>(smem + sizeof(Tile));
-  const int64_t ntok = (int64_t)a.B * a.L, n0 = (int64_t)blockIdx.x * tile;
-  const int count = ntok - n0 < tile ? (int)(ntok - n0) : tile;
-  fill_tile(a, t, cs, n0, count);
-
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rows = 32 / lanes, g = lane / lanes, lu = lane % lanes;
-  const int np = a.rope.dims / 2, inter = a.rope.interleaved;
-  const int per = rows * U, blocks = (count + per - 1) / per;
-  const int h0 = blockIdx.y * hchunk;
-  const int nh = a.set[0].heads + a.set[1].heads - h0 < hchunk
-                     ? a.set[0].heads + a.set[1].heads - h0 : hchunk;
-  bool bad = false;
-  for (int it = warp; it < nh * blocks; it += kWarps) {
-    const int hh = h0 + it / blocks, k0 = (it % blocks) * per;
-    const int which = hh >= a.set[0].heads ? 1 : 0;
-    const RowSet& rs = a.set[which];
-    const int h = hh - (which ? a.set[0].heads : 0);
-    const T* x = (const T*)rs.x + (int64_t)h * rs.xs[1];
-    const int rot = rs.rotate ? a.rope.dims : 0;
-    const float* gamma =
-        rs.gamma == nullptr ? nullptr : rs.gamma + (rs.gheads > 1 ? (int64_t)h * a.d : 0);
-    Pack<T, N> lo[U][NU], hi[U][NU];
+    fetch_commit();
+  };
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int k = k0 + u * rows + g;
-      if (k < count && !(a.lens != nullptr && t.tok[k].row < 0)) {
-        const T* src = x + (int64_t)t.tok[k].b * rs.xs[0] + (int64_t)t.tok[k].l * rs.xs[2];
+  for (int i = 0; i < S - 1; ++i) issue(slots + i * kStage);
+
+  Angles<N> cs[NU];
+  if (a.rope.dims > 0) {
+    const int64_t pos = !live ? 0 : a.positions != nullptr ? (int64_t)a.positions[n] : a.pos0 + place;
+#pragma unroll
+    for (int e = 0; e < NU; ++e) {
+      const int p0 = N * (lu + e * lanes);
+      if (2 * p0 < a.rope.dims) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) angle(pos, turns[p0 + j], &cs[e].c[j], &cs[e].s[j]);
+      }
+    }
+  }
+  Seen seen;
+  const float inv_d = 1.f / (float)a.d;
+  F2 gm[NU][N];
+#pragma unroll
+  for (int e = 0; e < NU; ++e)
+#pragma unroll
+    for (int i = 0; i < N; ++i) gm[e][i] = F2(0.f);
+  uint32_t at = 0, fill = (S - 1) * kStage;                // bytes into the ring
+  int hh = first;
+#pragma unroll 1
+  for (; w < 2; ++w) {                                     // (from here on: the consumer's set)
+    const int base = w ? heads0 : 0, end = min(last, base + a.set[w].heads);
+    if (hh >= end) continue;
+    const bool normed = a.set[w].gamma != nullptr, each = a.set[w].gheads > 1;
+    const bool rotate = a.set[w].rotate && a.rope.dims > 0;
+    const float* gamma = a.set[w].gamma + (each ? (int64_t)(hh - base) * a.d : 0);
+    T* y = y_of(w, hh - base);
+    const int64_t yh = APPEND ? (int64_t)a.page * a.d : a.set[w].ys[1];
+    bool fresh = normed;                                   // weights still to be loaded
+#pragma unroll 1
+    for (; hh < end; ++hh, y += yh) {
+      fetch_wait<S - 2>();
+      R lo[NU], hi[NU];
+#pragma unroll
+      for (int e = 0; e < NU; ++e) {
+        const uint8_t* src = &ring[warp][0][0][0][lane * R::kBytes] + at + 2 * e * kRun;
+        lo[e].load(reinterpret_cast<const T*>(src));
+        hi[e].load(reinterpret_cast<const T*>(src + kRun));
+      }
+      issue(slots + fill);                                 // the slot read last time round
+      fill = at;
+      at = at + kStage == S * kStage ? 0 : at + kStage;
+      if (normed || rotate) {                              // a plain copy keeps the bits
+        F2 v[NU][N], s2(0.f);
+#pragma unroll
+        for (int e = 0; e < NU; ++e) widen<T, N>(v[e], lo[e], hi[e]);
+        if (normed) {
+          if (fresh) {
+#pragma unroll
+            for (int e = 0; e < NU; ++e)
+              if (has[e]) load_weights<N>(gm[e], gamma + lo_at[e], gamma + hi_at[e]);
+            gamma += a.d;
+            fresh = each;
+          }
+#pragma unroll
+          for (int e = 0; e < NU; ++e)
+#pragma unroll
+            for (int i = 0; i < N; ++i) s2 = fma2(v[e][i], v[e][i], s2);
+          float ss = s2.sum();
+          for (int o = lanes >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          seen.add(ss);                                    // a sum of squares past fp32
+          const F2 rstd(rsqrtf(fmaf(ss, inv_d, a.eps)));
+#pragma unroll
+          for (int e = 0; e < NU; ++e)
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[e][i] = mul2(v[e][i], mul2(rstd, gm[e][i]));
+        }
 #pragma unroll
         for (int e = 0; e < NU; ++e) {
-          const int i = lu + e * lanes;
-          if (2 * N * i < a.d) {
-            const Unit<N> un(i, rot, inter);
-            load(lo[u][e], src + un.lo);
-            load(hi[u][e], src + un.hi);
-          }
+          if (rotate && 2 * N * (lu + e * lanes) < a.rope.dims) turn<N, INTER>(v[e], cs[e]);
+          narrow<T, N>(lo[e], hi[e], v[e], seen);
         }
       }
-    }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int k = k0 + u * rows + g;
-      const bool live = k < count && !(a.lens != nullptr && t.tok[k].row < 0);
-      T* dst = nullptr;
-      if (live)
-        dst = a.lens != nullptr
-                  ? (T*)rs.y + (t.tok[k].row + (int64_t)h * a.page) * a.d
-                  : (T*)rs.y + (int64_t)h * rs.ys[1] + (int64_t)t.tok[k].b * rs.ys[0] +
-                        (int64_t)t.tok[k].l * rs.ys[2];
-      if (gamma == nullptr && rot == 0) {            // a plain copy keeps the bits
-        if (live) {
-#pragma unroll
-          for (int e = 0; e < NU; ++e) {
-            const int i = lu + e * lanes;
-            if (2 * N * i < a.d) {
-              store(dst + 2 * N * i, lo[u][e]);
-              store(dst + 2 * N * i + N, hi[u][e]);
-            }
-          }
+      for (int e = 0; e < NU; ++e)
+        if (has[e]) {
+          lo[e].store(y + lo_at[e]);
+          hi[e].store(y + hi_at[e]);
         }
-        continue;
-      }
-      float v[NU][2 * N], ss = 0.f;
-#pragma unroll
-      for (int e = 0; e < NU; ++e) {
-        const bool has = live && 2 * N * (lu + e * lanes) < a.d;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          v[e][i] = has ? to_f32(lo[u][e].v[i]) : 0.f;
-          v[e][N + i] = has ? to_f32(hi[u][e].v[i]) : 0.f;
-          ss = fmaf(v[e][i], v[e][i], ss);
-          ss = fmaf(v[e][N + i], v[e][N + i], ss);
-        }
-      }
-      float rstd = 1.f;
-      if (gamma != nullptr) {
-        ss = group_sum(ss, lanes);
-        rstd = 1.f / sqrtf(ss / (float)a.d + a.eps);
-        bad |= live && !isfinite(ss);                // a sum of squares past fp32
-      }
-      if (!live) continue;
-#pragma unroll
-      for (int e = 0; e < NU; ++e) {
-        const int i = lu + e * lanes;
-        if (2 * N * i >= a.d) continue;
-        const Unit<N> un(i, rot, inter);
-        if (gamma != nullptr) {
-          Pack<float, N> glo, ghi;
-          load(glo, gamma + un.lo);
-          load(ghi, gamma + un.hi);
-#pragma unroll
-          for (int j = 0; j < N; ++j) {
-            v[e][j] *= rstd * glo.v[j];
-            v[e][N + j] *= rstd * ghi.v[j];
-          }
-        }
-        if (un.pair >= 0) turn<N>(v[e], cs + k * np + un.pair, inter, 1.f);
-        Pack<T, N> olo, ohi;
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-          bad |= !isfinite(v[e][j]) || !isfinite(v[e][N + j]);
-          olo.v[j] = from_f32<T>(v[e][j]);
-          ohi.v[j] = from_f32<T>(v[e][N + j]);
-        }
-        store(dst + un.lo, olo);
-        store(dst + un.hi, ohi);
-      }
     }
   }
-  if (bad) report(a.dev_status, DARK_ERR_NUMERIC);
+  if (seen.bad()) report(a.dev_status, DARK_ERR_NUMERIC);
 }
 
-// Backward. blockIdx.y is a group of at most kWarps heads, a warp keeps one head
-// (with fewer heads, several warps share one and split its tokens), and a CTA walks
-// tiles blockIdx.x, blockIdx.x + gridDim.x, ...: dgamma stays in registers, one sum a
-// tile added to one over the tiles (two levels: the fp32 sums stay short), and each
-// warp leaves one row for the reduction below.
-template <typename T, int N, int NU>
-__global__ void __launch_bounds__(kThreads) rows_bwd_kernel(const __grid_constant__ NormRopeArgs a,
-                                                            int lanes, int tile) {
-  constexpr int U = NU > 1 ? 1 : 2;
+// Partial rows of dgamma: for a shared weight one of every CTA that holds heads of the set
+// (head groups `group`, `group` + 1, ...), else `ctas * split` of every head.
+struct PartRows {
+  int64_t first;                          // of the set
+  int rows, group;                        // rows of one output row; the set's first head group
+};
+__device__ __forceinline__ int head_split(int nh) { return nh < kWarps ? kWarps / nh : 1; }
+__device__ __forceinline__ PartRows part_rows(const NormRopeArgs& a, int set, int ctas) {
+  const int h0 = a.set[0].heads, nh = h0 + a.set[1].heads;
+  const int lo = set ? h0 : 0, hi = set ? nh : h0;
+  PartRows p;
+  p.first = set ? (int64_t)h0 * ctas * head_split(nh) : 0;
+  p.group = lo / kWarps;
+  p.rows = a.set[set].gheads > 1 ? ctas * head_split(nh) : ((hi - 1) / kWarps - p.group + 1) * ctas;
+  return p;
+}
+
+// Backward. blockIdx.y is a group of at most kWarps heads, a warp keeps one head (with
+// fewer heads, several warps share one and split its tokens) and its weights and dgamma
+// in registers. A CTA walks its `span` tokens; the rows of its warps stream through S slots
+// of shared memory a lane, and the cosines and sines of `tile` tokens at a time lie in
+// shared memory for all its heads: pairs 2 j, 2 j + 1 of unit u of token k as one float4
+// (two cosines, two sines) at (j tile + k) units + u, so that the lanes of a warp read
+// consecutive 16-byte words. Each warp leaves one row of sums for the reduction below.
+template <typename T, int N, int NU, int S, bool INTER>
+__global__ void __launch_bounds__(kThreads, 2) rows_bwd_kernel(const __grid_constant__ NormRopeArgs a,
+                                                               int lanes, int span, int tile) {
+  using R = Run<T, N>;
+  constexpr int NC = N > 1 ? N / 2 : 1, PC = N > 1 ? 2 : 1;
+  constexpr uint32_t kRun = 32 * R::kBytes, kStage = NU * 4 * kRun;
   extern __shared__ __align__(16) uint8_t smem[];
-  Tile& t = *reinterpret_cast<Tile*>(smem);
-  float2* cs = reinterpret_cast<float2*>(smem + sizeof(Tile));
+  __shared__ uint64_t turns[128];
+  float* cs = reinterpret_cast<float*>(smem + kWarps * S * kStage);
+  pdl_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rows = 32 / lanes, g = lane / lanes, lu = lane % lanes;
-  const int np = a.rope.dims / 2, inter = a.rope.interleaved;
+  const int np = a.rope.dims / 2, units = np / N;
   const int nh = a.set[0].heads + a.set[1].heads;
-  const int h0 = blockIdx.y * kWarps;
   const int hg = nh < kWarps ? nh : kWarps, split = kWarps / hg;
-  const int hh = h0 + warp % hg, part = warp / hg;
+  const int hh = blockIdx.y * kWarps + warp % hg, part = warp / hg;
   const bool on = hh < nh && part < split;
   const int which = hh >= a.set[0].heads ? 1 : 0;
   const RowSet& rs = a.set[which];
   const int h = hh - (which ? a.set[0].heads : 0);
-  const int rot = rs.rotate ? a.rope.dims : 0;
-  const float* gamma =
-      rs.gamma == nullptr ? nullptr : rs.gamma + (rs.gheads > 1 ? (int64_t)h * a.d : 0);
-  float sum[NU][2 * N];
+  const int rot = a.rope.dims;
+  const bool normed = rs.gamma != nullptr;
+  const T* xh = (const T*)rs.x + (int64_t)h * rs.xs[1];
+  const T* gh = (const T*)rs.g + (int64_t)h * rs.gs[1];
+  T* yh = (T*)rs.y + (int64_t)h * rs.ys[1];
+  const uint32_t ntok = (uint32_t)a.B * a.L, t0 = blockIdx.x * span;
+  const int count = t0 < ntok ? (int)min((uint32_t)span, ntok - t0) : 0;
+  bool has[NU];
+#pragma unroll
+  for (int e = 0; e < NU; ++e) has[e] = 2 * N * (lu + e * lanes) < a.d;
+
+  int lo_at[NU], hi_at[NU];
+#pragma unroll
+  for (int e = 0; e < NU; ++e) {
+    const Unit<N, INTER> un(lu + e * lanes, rot);
+    lo_at[e] = un.lo;
+    hi_at[e] = un.hi;
+  }
+  uint8_t* ring = smem + warp * S * kStage + lane * R::kBytes;
+  const uint32_t slots = (uint32_t)__cvta_generic_to_shared(ring);
+  const int step = split * rows, mine = part * rows + g;   // tokens mine, mine + step, ...
+  // rows of the next token to fetch, moved on by `step` tokens at a time
+  int next = mine, next_l = 0;
+  const T *xr = nullptr, *gr = nullptr;
+  auto seek = [&]() {
+    const uint32_t n = t0 + next, b = n / a.L;
+    next_l = n - b * a.L;
+    xr = xh + (int64_t)b * rs.xs[0] + next_l * rs.xs[2];
+    gr = gh + (int64_t)b * rs.gs[0] + next_l * rs.gs[2];
+  };
+  seek();
+  const int64_t x_step = step * rs.xs[2], g_step = step * rs.gs[2], y_step = step * rs.ys[2];
+  auto issue = [&](uint32_t slot) {
+    const bool ok = on && next < count;
+#pragma unroll
+    for (int e = 0; e < NU; ++e) {
+      const uint32_t to = slot + 4 * e * kRun;
+      fetch<T, N>(to, xr + lo_at[e], ok && has[e] && normed);
+      fetch<T, N>(to + kRun, xr + hi_at[e], ok && has[e] && normed);
+      fetch<T, N>(to + 2 * kRun, gr + lo_at[e], ok && has[e]);
+      fetch<T, N>(to + 3 * kRun, gr + hi_at[e], ok && has[e]);
+    }
+    fetch_commit();
+    next += step;
+    next_l += step;
+    xr += x_step;
+    gr += g_step;
+    if (next_l >= a.L) seek();
+  };
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) issue(slots + i * kStage);
+
+  F2 acc[NU][N], gm[NU][N];
+#pragma unroll
+  for (int e = 0; e < NU; ++e) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) acc[e][j] = gm[e][j] = F2(0.f);
+    if (on && normed && has[e]) {
+      const float* src = rs.gamma + (rs.gheads > 1 ? (int64_t)h * a.d : 0);
+      load_weights<N>(gm[e], src + lo_at[e], src + hi_at[e]);
+    }
+  }
+  if (threadIdx.x < np) turns[threadIdx.x] = a.rope.turns[threadIdx.x];
+  Seen seen;
+  const float inv_d = 1.f / (float)a.d;
+  uint32_t from = 0, fill = (S - 1) * kStage;        // bytes into the ring
+  int k = mine;                                      // this lane group's next token
+  int at_l = a.L;                                    // its row of results (found when needed)
+  T* dst = nullptr;
+  for (int tile0 = 0; tile0 < count; tile0 += tile) {
+    const int here = min(tile, count - tile0);
+    __syncthreads();                                 // turns; the last tile's readers are done
+    for (int kk = warp; kk < here; kk += kWarps) {
+      const uint32_t n = t0 + tile0 + kk;
+      const int64_t pos = a.positions != nullptr ? (int64_t)a.positions[n] : a.pos0 + n % a.L;
+      for (int p = lane; p < np; p += 32) {
+        const int u = p / N, j = p % N / PC;
+        float* to = cs + ((j * tile + kk) * units + u) * 2 * PC + p % PC;
+        angle(pos, turns[p], to, to + PC);
+      }
+    }
+    __syncthreads();
+    if (!on) continue;
+    // a warp's groups are `rows` apart at most and tiles are multiples of `step`: all leave
+    // the loop together
+#pragma unroll 1
+    for (; k - g < tile0 + here; k += step) {
+      fetch_wait<S - 2>();
+      const bool live = k < count;
+      R lo[NU], hi[NU];
+      F2 x[NU][N], w[NU][N], ss2(0.f), dot2(0.f);
+#pragma unroll
+      for (int e = 0; e < NU; ++e) {
+        const uint8_t* src = ring + from + 4 * e * kRun;
+        lo[e].load(reinterpret_cast<const T*>(src));
+        hi[e].load(reinterpret_cast<const T*>(src + kRun));
+        widen<T, N>(x[e], lo[e], hi[e]);
+        lo[e].load(reinterpret_cast<const T*>(src + 2 * kRun));
+        hi[e].load(reinterpret_cast<const T*>(src + 3 * kRun));
+        widen<T, N>(w[e], lo[e], hi[e]);
+      }
+      issue(slots + fill);                           // the slot read last time round
+      fill = from;
+      from = from + kStage == S * kStage ? 0 : from + kStage;
+#pragma unroll
+      for (int e = 0; e < NU; ++e) {
+        const int i = lu + e * lanes;
+        if (live && 2 * N * i < rot) {               // w = u, the cotangent turned back
+          Angles<N> t;
+#pragma unroll
+          for (int j = 0; j < NC; ++j) {
+            const float* src = cs + ((j * tile + k - tile0) * units + i) * 2 * PC;
+            if constexpr (N > 1) {
+              const float4 v = *reinterpret_cast<const float4*>(src);
+              t.c[2 * j] = v.x;
+              t.c[2 * j + 1] = v.y;
+              t.s[2 * j] = -v.z;
+              t.s[2 * j + 1] = -v.w;
+            } else {
+              t.c[0] = src[0];
+              t.s[0] = -src[1];
+            }
+          }
+          turn<N, INTER>(w[e], t);
+        }
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          ss2 = fma2(x[e][j], x[e][j], ss2);
+          dot2 = fma2(mul2(w[e][j], gm[e][j]), x[e][j], dot2);
+        }
+      }
+      if (normed) {
+        float ss = ss2.sum(), dot = dot2.sum();
+        for (int o = lanes >> 1; o > 0; o >>= 1) {
+          ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          dot += __shfl_xor_sync(0xffffffffu, dot, o);
+        }
+        seen.add(ss);
+        const float r = rsqrtf(fmaf(ss, inv_d, a.eps));
+        const F2 rstd(r), back(-dot * inv_d * r * r * r);        // -mean(w n) rstd^2
+#pragma unroll
+        for (int e = 0; e < NU; ++e)
+#pragma unroll
+          for (int j = 0; j < N; ++j) {
+            const F2 wr = mul2(w[e][j], rstd);
+            acc[e][j] = fma2(wr, x[e][j], acc[e][j]);
+            w[e][j] = fma2(wr, gm[e][j], mul2(x[e][j], back));
+          }
+      }
+      if (at_l >= a.L) {
+        const uint32_t n = t0 + k, b = n / a.L;
+        at_l = n - b * a.L;
+        dst = yh + (int64_t)b * rs.ys[0] + at_l * rs.ys[2];
+      }
+#pragma unroll
+      for (int e = 0; e < NU; ++e) {
+        narrow<T, N>(lo[e], hi[e], w[e], seen);
+        if (live && has[e]) {
+          lo[e].store(dst + lo_at[e]);
+          hi[e].store(dst + hi_at[e]);
+        }
+      }
+      dst += y_step;
+      at_l += step;
+    }
+  }
+  fetch_wait<0>();
+  if (seen.bad()) report(a.dev_status, DARK_ERR_NUMERIC);
+  // the warps' rows of sums in shared memory (in the place of the rings and angles)
+  __syncthreads();
+  float* sums = reinterpret_cast<float*>(smem);      // [warp][d]
 #pragma unroll
   for (int e = 0; e < NU; ++e)
 #pragma unroll
-    for (int j = 0; j < 2 * N; ++j) sum[e][j] = 0.f;
-  bool bad = false;
-
-  const int64_t ntok = (int64_t)a.B * a.L;
-  for (int64_t n0 = (int64_t)blockIdx.x * tile; n0 < ntok; n0 += (int64_t)gridDim.x * tile) {
-    const int count = ntok - n0 < tile ? (int)(ntok - n0) : tile;
-    __syncthreads();                                 // the last tile's readers are done
-    fill_tile(a, t, cs, n0, count);
-    if (!on) continue;
-    float acc[NU][2 * N];
-#pragma unroll
-    for (int e = 0; e < NU; ++e)
-#pragma unroll
-      for (int j = 0; j < 2 * N; ++j) acc[e][j] = 0.f;
-    for (int k0 = part * rows * U; k0 < count; k0 += split * rows * U) {
-      Pack<T, N> xlo[U][NU], xhi[U][NU], glo[U][NU], ghi[U][NU];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int k = k0 + u * rows + g;
-        if (k >= count) continue;
-        const int64_t tb = t.tok[k].b, tl = t.tok[k].l;
-        const T* xr = (const T*)rs.x + (int64_t)h * rs.xs[1] + tb * rs.xs[0] + tl * rs.xs[2];
-        const T* gr = (const T*)rs.g + (int64_t)h * rs.gs[1] + tb * rs.gs[0] + tl * rs.gs[2];
-#pragma unroll
-        for (int e = 0; e < NU; ++e) {
-          const int i = lu + e * lanes;
-          if (2 * N * i >= a.d) continue;
-          const Unit<N> un(i, rot, inter);
-          if (gamma != nullptr) {
-            load(xlo[u][e], xr + un.lo);
-            load(xhi[u][e], xr + un.hi);
-          }
-          load(glo[u][e], gr + un.lo);
-          load(ghi[u][e], gr + un.hi);
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int k = k0 + u * rows + g;
-        const bool live = k < count;
-        float x[NU][2 * N], w[NU][2 * N], ss = 0.f, dot = 0.f;
-#pragma unroll
-        for (int e = 0; e < NU; ++e) {
-          const int i = lu + e * lanes;
-          const bool has = live && 2 * N * i < a.d;
-          const Unit<N> un(i, rot, inter);
-#pragma unroll
-          for (int j = 0; j < N; ++j) {
-            x[e][j] = has && gamma != nullptr ? to_f32(xlo[u][e].v[j]) : 0.f;
-            x[e][N + j] = has && gamma != nullptr ? to_f32(xhi[u][e].v[j]) : 0.f;
-            w[e][j] = has ? to_f32(glo[u][e].v[j]) : 0.f;
-            w[e][N + j] = has ? to_f32(ghi[u][e].v[j]) : 0.f;
-          }
-          if (has && un.pair >= 0) turn<N>(w[e], cs + k * np + un.pair, inter, -1.f);   // u
-          if (has && gamma != nullptr) {
-            Pack<float, N> mlo, mhi;
-            load(mlo, gamma + un.lo);
-            load(mhi, gamma + un.hi);
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-              ss = fmaf(x[e][j], x[e][j], ss);
-              ss = fmaf(x[e][N + j], x[e][N + j], ss);
-              dot = fmaf(w[e][j] * mlo.v[j], x[e][j], dot);
-              dot = fmaf(w[e][N + j] * mhi.v[j], x[e][N + j], dot);
-            }
-          }
-        }
-        float rstd = 1.f, back = 0.f;
-        if (gamma != nullptr) {
-          ss = group_sum(ss, lanes);
-          dot = group_sum(dot, lanes);
-          rstd = 1.f / sqrtf(ss / (float)a.d + a.eps);
-          back = dot * rstd * rstd / (float)a.d;     // mean(w n) rstd
-          bad |= live && !isfinite(ss);
-        }
-        if (!live) continue;
-        T* dr = (T*)rs.y + (int64_t)h * rs.ys[1] + (int64_t)t.tok[k].b * rs.ys[0] +
-                (int64_t)t.tok[k].l * rs.ys[2];
-#pragma unroll
-        for (int e = 0; e < NU; ++e) {
-          const int i = lu + e * lanes;
-          if (2 * N * i >= a.d) continue;
-          const Unit<N> un(i, rot, inter);
-          float dx[2 * N];
-          if (gamma != nullptr) {
-            Pack<float, N> mlo, mhi;
-            load(mlo, gamma + un.lo);
-            load(mhi, gamma + un.hi);
-#pragma unroll
-            for (int j = 0; j < 2 * N; ++j) {
-              const float m = j < N ? mlo.v[j % N] : mhi.v[j % N];
-              acc[e][j] = fmaf(w[e][j], x[e][j] * rstd, acc[e][j]);
-              dx[j] = rstd * fmaf(-x[e][j], back, w[e][j] * m);
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 2 * N; ++j) dx[j] = w[e][j];
-          }
-          Pack<T, N> olo, ohi;
-#pragma unroll
-          for (int j = 0; j < N; ++j) {
-            bad |= !isfinite(dx[j]) || !isfinite(dx[N + j]);
-            olo.v[j] = from_f32<T>(dx[j]);
-            ohi.v[j] = from_f32<T>(dx[N + j]);
-          }
-          store(dr + un.lo, olo);
-          store(dr + un.hi, ohi);
-        }
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < NU; ++e)
-#pragma unroll
-      for (int j = 0; j < 2 * N; ++j) sum[e][j] += acc[e][j];
-  }
-  if (bad) report(a.dev_status, DARK_ERR_NUMERIC);
-  if (!on || gamma == nullptr) return;
-  // the warp's row of partial sums: [head][slot][d]
-  float* out = a.part + ((int64_t)hh * gridDim.x * split + (int64_t)blockIdx.x * split + part) * a.d;
-#pragma unroll
-  for (int e = 0; e < NU; ++e) {
-    const int i = lu + e * lanes;
-    const Unit<N> un(i, rot, inter);
-#pragma unroll
     for (int j = 0; j < 2 * N; ++j) {
-      float v = sum[e][j];
+      const int i = N == 1 ? 0 : j / 2;              // value j of (lo run, hi run)
+      float v = j % 2 == 0 ? acc[e][i].get().x : acc[e][i].get().y;
       for (int o = lanes; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      if (g == 0 && 2 * N * i < a.d) out[(j < N ? un.lo : un.hi - N) + j] = v;
+      if (g == 0 && has[e]) sums[warp * a.d + (j < N ? lo_at[e] : hi_at[e] - N) + j] = v;
     }
-  }
+  __syncthreads();
+  // one partial row for every set with a shared weight, or one for every head
+  for (int c = threadIdx.x; c < a.d; c += kThreads)
+    for (int s = 0; s < 2; ++s) {
+      const RowSet& r = a.set[s];
+      if (r.gamma == nullptr) continue;
+      const PartRows pr = part_rows(a, s, gridDim.x);
+      const int base = s ? a.set[0].heads : 0;
+      float v = 0.f;
+      bool any = false;
+      for (int i = 0; i < kWarps; ++i) {
+        const int hi = blockIdx.y * kWarps + i % hg, p = i / hg;
+        if (hi >= nh || p >= split || hi < base || hi >= base + r.heads) continue;
+        any = true;
+        v += sums[i * a.d + c];
+        if (r.gheads > 1) {
+          a.part[(pr.first + ((int64_t)(hi - base) * gridDim.x + blockIdx.x) * split + p) * a.d + c] = v;
+          v = 0.f;
+        }
+      }
+      if (any && r.gheads == 1)
+        a.part[(pr.first + (int64_t)(blockIdx.y - pr.group) * gridDim.x + blockIdx.x) * a.d + c] = v;
+    }
 }
 
-// dgamma rows from the warps' partial rows, in a fixed order and fp64: 32 columns of
-// one output row a CTA, warps over the partial rows. blockIdx.y: the output rows of q,
-// then of k; a shared gamma's row sums the partial rows of all its heads.
-__global__ void __launch_bounds__(1024) dgamma_kernel(const __grid_constant__ NormRopeArgs a,
-                                                      int slots) {
-  __shared__ double red[32][33];
+// dgamma rows from the partial rows, in a fixed order and fp64: 32 columns of one output
+// row a CTA, warps over the partial rows. blockIdx.y: the output rows of q, then of k.
+__global__ void __launch_bounds__(512) dgamma_kernel(const __grid_constant__ NormRopeArgs a, int ctas) {
+  constexpr int kW = 16;
+  __shared__ double red[kW][33];
+  pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   const int q_rows = a.set[0].gamma == nullptr ? 0 : a.set[0].gheads;
   const int which = (int)blockIdx.y >= q_rows ? 1 : 0;
   const RowSet& rs = a.set[which];
   const int o = blockIdx.y - (which ? q_rows : 0);
-  const int64_t nrows = (int64_t)slots * (rs.gheads > 1 ? 1 : rs.heads);
-  const int64_t first = (which ? (int64_t)a.set[0].heads * slots : 0) + o * nrows;
+  const PartRows pr = part_rows(a, which, ctas);
   double s = 0.0;
   if (c < a.d) {
-    const float* src = a.part + first * a.d + c;
-    int64_t i = warp;
-    for (; i + 7 * 32 < nrows; i += 8 * 32) {
+    const float* src = a.part + (pr.first + (int64_t)o * pr.rows) * a.d + c;
+    int i = warp;
+    for (; i + 7 * kW < pr.rows; i += 8 * kW) {
       float v[8];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) v[u] = src[(i + u * 32) * a.d];
+      for (int u = 0; u < 8; ++u) v[u] = src[(int64_t)(i + u * kW) * a.d];
 #pragma unroll
       for (int u = 0; u < 8; ++u) s += v[u];
     }
-    for (; i < nrows; i += 32) s += src[i * a.d];
+    for (; i < pr.rows; i += kW) s += src[(int64_t)i * a.d];
   }
   red[warp][lane] = s;
   __syncthreads();
   if (warp == 0 && c < a.d) {
     double r = 0.0;
-    for (int w = 0; w < 32; ++w) r += red[w][lane];
+    for (int w = 0; w < kW; ++w) r += red[w][lane];
     rs.dgamma[(int64_t)o * a.d + c] = (float)r;
     if (!isfinite(r)) report(a.dev_status, DARK_ERR_NUMERIC);
   }
 }
 
-// Four pairs a unit (8- or 16-byte accesses) need eight-element multiples and
-// aligned rows; every other layout takes one pair a unit with scalar accesses.
-bool vector_ok(const NormRopeArgs& a) {
-  const size_t al = a.dtype == DARK_BF16 ? 8 : 16;
-  auto ok = [&](const void* p, const int64_t* s) {
-    return p == nullptr || ((uintptr_t)p % al == 0 && s[0] % 4 == 0 && s[1] % 4 == 0 && s[2] % 4 == 0);
+// Pairs of a unit: the largest run whose accesses (up to 16 bytes) all rows, strides and
+// weights are aligned for. Narrower units hold their rows in several units a lane.
+int pairs_for(const NormRopeArgs& a) {
+  const size_t e = a.dtype == DARK_BF16 ? 2 : 4;
+  auto fits = [&](int n) {
+    if (a.d % (2 * n) != 0 || a.rope.dims % (2 * n) != 0) return false;
+    auto ok = [&](const void* p, const int64_t* s) {
+      return p == nullptr || ((uintptr_t)p % (n * e) == 0 && s[0] % n == 0 && s[1] % n == 0 &&
+                              s[2] % n == 0);
+    };
+    for (int i = 0; i < 2; ++i) {
+      const RowSet& s = a.set[i];
+      if (!ok(s.x, s.xs) || !ok(s.y, s.ys) || !ok(s.g, s.gs)) return false;
+      if (n >= 4 && (uintptr_t)s.gamma % 16 != 0) return false;
+    }
+    return true;
   };
-  if (a.d % 8 != 0 || a.rope.dims % 8 != 0) return false;
-  for (int i = 0; i < 2; ++i) {
-    const RowSet& s = a.set[i];
-    if (!ok(s.x, s.xs) || !ok(s.y, s.ys) || !ok(s.g, s.gs)) return false;
-    if ((uintptr_t)s.gamma % 16 != 0) return false;
-  }
-  return true;
+  if (a.dtype == DARK_BF16 && fits(8)) return 8;
+  return fits(4) ? 4 : fits(2) ? 2 : 1;
 }
 
 int lanes_for(int d, int pairs) {
@@ -481,60 +714,80 @@ int lanes_for(int d, int pairs) {
   return l;
 }
 
-template <typename T>
+// Units a lane needs for d = 256 in 32 lanes.
+constexpr int units_of(int n) { return n >= 4 ? 1 : 4 / n; }
+
+template <typename T, int N, bool INTER>
 cudaError_t launch_rows(const NormRopeArgs& a) {
-  const bool vec = vector_ok(a);
-  const int lanes = lanes_for(a.d, vec ? 4 : 1), rows = 32 / lanes;
+  constexpr int NU = units_of(N), S = NU == 1 ? 6 : 3;
+  const int lanes = lanes_for(a.d, N), rows = 32 / lanes;
   const int nh = a.set[0].heads + a.set[1].heads;
-  const int64_t ntok = (int64_t)a.B * a.L;
-  // tiles of 32 tokens and all heads in a CTA; with too little work for two CTAs
-  // an SM first smaller tiles, then fewer heads
-  int tile = kTile, hchunk = nh;
-  auto ctas = [&]() { return (ntok + tile - 1) / tile * ((nh + hchunk - 1) / hchunk); };
-  while (tile > rows && ctas() < 2 * num_sms()) tile /= 2;
-  while (hchunk > 1 && (int64_t)hchunk * tile > (int64_t)rows * kWarps && ctas() < 2 * num_sms())
-    hchunk = (hchunk + 1) / 2;
+  const int64_t groups = ((int64_t)a.B * a.L + rows - 1) / rows;
+  const int64_t x = (groups + kRowWarps - 1) / kRowWarps;
+  // all heads of a token in one warp (its angles are computed once), unless that leaves
+  // SMs without two CTAs
+  int hchunk = nh;
+  while (hchunk > 1 && x * ((nh + hchunk - 1) / hchunk) < 2 * num_sms()) hchunk = (hchunk + 1) / 2;
   while ((nh + hchunk - 1) / hchunk > 65535) hchunk *= 2;
-  const dim3 grid((unsigned)((ntok + tile - 1) / tile), (nh + hchunk - 1) / hchunk);
-  const size_t smem = sizeof(Tile) + (size_t)tile * (a.rope.dims / 2) * sizeof(float2);
-  if (vec)
-    rows_kernel<T, 4, 1, 4><<<grid, kThreads, smem, a.stream>>>(a, lanes, tile, hchunk);
+  const dim3 grid((unsigned)x, (nh + hchunk - 1) / hchunk);
+  if (a.lens != nullptr)
+    rows_kernel<T, N, NU, S, INTER, true><<<grid, 32 * kRowWarps, 0, a.stream>>>(a, lanes, hchunk);
   else
-    rows_kernel<T, 1, 4, 1><<<grid, kThreads, smem, a.stream>>>(a, lanes, tile, hchunk);
+    rows_kernel<T, N, NU, S, INTER, false><<<grid, 32 * kRowWarps, 0, a.stream>>>(a, lanes, hchunk);
   return cudaGetLastError();
 }
 
-// CTAs along the tokens of the backward pass: at most four an SM over all head
-// groups, and a tile each.
+// CTAs along the tokens of the backward pass: two an SM over all head groups, and 16
+// tokens each at least.
 int bwd_ctas(int64_t ntok, int nh) {
   const int groups = (nh + kWarps - 1) / kWarps;
-  const int64_t tiles = (ntok + kTile - 1) / kTile;
-  const int64_t most = 592 / groups > 0 ? 592 / groups : 1;
-  return (int)(tiles < most ? tiles : most);
+  const int64_t least = (ntok + 15) / 16;
+  const int64_t most = 296 / groups > 0 ? 296 / groups : 1;
+  return (int)(least < most ? least : most);
 }
 int bwd_split(int nh) { return nh < kWarps ? kWarps / nh : 1; }
 
-template <typename T>
+template <typename T, int N, bool INTER>
 cudaError_t launch_rows_bwd(const NormRopeArgs& a) {
-  const bool vec = vector_ok(a);
-  const int lanes = lanes_for(a.d, vec ? 4 : 1);
-  const int nh = a.set[0].heads + a.set[1].heads;
+  constexpr int NU = units_of(N), S = NU == 1 ? 4 : 3;
+  static int smem_set[64];
+  const int lanes = lanes_for(a.d, N);
+  const int nh = a.set[0].heads + a.set[1].heads, np = a.rope.dims / 2;
   const int64_t ntok = (int64_t)a.B * a.L;
-  const int ctas = bwd_ctas(ntok, nh);
-  // even tiles: with few tokens every CTA gets some
-  int64_t per = (ntok + ctas - 1) / ctas;
-  const int tile = per < kTile ? (int)per : kTile;
+  const int ctas = bwd_ctas(ntok, nh), step = 32 / lanes * bwd_split(nh);
+  const int span = (int)((ntok + ctas - 1) / ctas);
+  // angles of at most 32 KB at a time; tiles a multiple of the tokens of one step
+  const int most = (np == 0 ? span : 4096 / np) / step * step;
+  const int tile = most < step ? step : most < span ? most : (span + step - 1) / step * step;
+  const size_t ring = (size_t)kWarps * S * NU * 4 * 32 * N * sizeof(T);
+  const size_t smem = ring + (size_t)tile * a.rope.dims * sizeof(float);
+  auto* kernel = rows_bwd_kernel<T, N, NU, S, INTER>;
+  cudaError_t e = set_smem_limit_once((const void*)kernel, (int)(ring + 65536), smem_set);
+  if (e != cudaSuccess) return e;
   const dim3 grid(ctas, (nh + kWarps - 1) / kWarps);
-  const size_t smem = sizeof(Tile) + (size_t)tile * (a.rope.dims / 2) * sizeof(float2);
-  if (vec)
-    rows_bwd_kernel<T, 4, 1><<<grid, kThreads, smem, a.stream>>>(a, lanes, tile);
-  else
-    rows_bwd_kernel<T, 1, 4><<<grid, kThreads, smem, a.stream>>>(a, lanes, tile);
-  cudaError_t e = cudaGetLastError();
+  kernel<<<grid, kThreads, smem, a.stream>>>(a, lanes, span, tile);
+  e = cudaGetLastError();
   const int out_rows = (a.set[0].gamma ? a.set[0].gheads : 0) + (a.set[1].gamma ? a.set[1].gheads : 0);
   if (e != cudaSuccess || out_rows == 0) return e;
-  dgamma_kernel<<<dim3((a.d + 31) / 32, out_rows), 1024, 0, a.stream>>>(a, ctas * bwd_split(nh));
-  return cudaGetLastError();
+  return launch_dependent(dgamma_kernel, dim3((a.d + 31) / 32, out_rows), dim3(512), 0, a.stream, a, ctas);
+}
+
+// The instance for a call's type, unit width and pair layout.
+template <typename T, int N>
+cudaError_t launch_n(const NormRopeArgs& a, bool bwd) {
+  if (a.rope.interleaved) return bwd ? launch_rows_bwd<T, N, true>(a) : launch_rows<T, N, true>(a);
+  return bwd ? launch_rows_bwd<T, N, false>(a) : launch_rows<T, N, false>(a);
+}
+cudaError_t launch(const NormRopeArgs& a, bool bwd) {
+  const int n = pairs_for(a);
+  if (a.dtype == DARK_BF16)
+    return n == 8   ? launch_n<__nv_bfloat16, 8>(a, bwd)
+           : n == 4 ? launch_n<__nv_bfloat16, 4>(a, bwd)
+           : n == 2 ? launch_n<__nv_bfloat16, 2>(a, bwd)
+                    : launch_n<__nv_bfloat16, 1>(a, bwd);
+  return n == 4 ? launch_n<float, 4>(a, bwd)
+         : n == 2 ? launch_n<float, 2>(a, bwd)
+                  : launch_n<float, 1>(a, bwd);
 }
 
 }  // namespace
@@ -544,12 +797,7 @@ size_t norm_rope_bwd_workspace_bytes(int B, int H, int Hk, int L, int d) {
   return kWsHeader + align_up((size_t)nh * bwd_ctas((int64_t)B * L, nh) * bwd_split(nh) * d * 4, 256);
 }
 
-cudaError_t launch_norm_rope(const NormRopeArgs& a) {
-  return a.dtype == DARK_BF16 ? launch_rows<__nv_bfloat16>(a) : launch_rows<float>(a);
-}
-
-cudaError_t launch_norm_rope_bwd(const NormRopeArgs& a) {
-  return a.dtype == DARK_BF16 ? launch_rows_bwd<__nv_bfloat16>(a) : launch_rows_bwd<float>(a);
-}
+cudaError_t launch_norm_rope(const NormRopeArgs& a) { return launch(a, false); }
+cudaError_t launch_norm_rope_bwd(const NormRopeArgs& a) { return launch(a, true); }
 
 }  // namespace dark

@@ -9,6 +9,7 @@ module fails loudly if that library has not been built.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -66,6 +67,7 @@ class dark_kv_cache(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("pages", ctypes.c_int),
                 ("heads", ctypes.c_int), ("page_size", ctypes.c_int), ("d", ctypes.c_int),
                 ("dtype", ctypes.c_int)]
+    device = None                      # index of the tensors' device, where it is known
 
 
 _P = ctypes.POINTER
@@ -402,63 +404,79 @@ def dark_sample_omega(seed: int, draw: int, omega, orthogonal: bool = True, ws=N
 # tensors agree; what the C ABI checks (ranges, alignment, flags) stays there.
 
 _DTYPES = {torch.float32: DARK_F32, torch.bfloat16: DARK_BF16}
-_INT32, _F32 = (torch.int32,), (torch.float32,)
 
 
-def _want(t, name, shape, dtypes, dev):
-    """A dense tensor of the given shape, type and device."""
-    if t.shape != shape or t.dtype not in dtypes or t.device != dev or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous tensor of shape {tuple(shape)}, type "
-                         f"{' or '.join(str(x) for x in dtypes)} on {dev}")
-    return t.data_ptr()
+@functools.lru_cache(maxsize=4096)
+def _s3(b, h, l):
+    """Element strides {b, h, l} as the C ABI takes them (read-only there)."""
+    return (ctypes.c_int64 * 3)(b, h, l)
 
 
 def _rows(t, name, B, L, d, dtype, dev):
     """A [B][heads][L][d] tensor with a unit d stride: pointer, strides, heads."""
-    s = t.stride()
-    if t.dim() != 4 or t.shape[0] != B or t.shape[2] != L or t.shape[3] != d:
+    n, s = t.shape, t.stride()
+    if len(n) != 4 or n[0] != B or n[2] != L or n[3] != d:
         raise ValueError(f"{name}: expected [B][heads][L][d] = [{B}][..][{L}][{d}]")
-    if s[3] != 1 or t.dtype != dtype or t.device != dev:
-        raise ValueError(f"{name}: expected type {dtype} and a unit d stride, on {dev}")
-    return t.data_ptr(), _S3(s[0], s[1], s[2]), t.shape[1]
+    if s[3] != 1 or t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError(f"{name}: expected type {dtype} and a unit d stride, on q's device")
+    return t.data_ptr(), _s3(s[0], s[1], s[2]), n[1]
 
 
-_S3 = ctypes.c_int64 * 3
+def _want(t, name, shape, dtype, dev):
+    """The address of a dense tensor of the given shape, type and device; None: NULL."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor of shape {tuple(shape)} and type "
+                         f"{dtype}, on the same device")
+    return t.data_ptr()
 
 
 def _weight(g, name, heads, d, dev):
     """A norm weight [1 or heads][d] (or [d]): pointer, rows; None: (None, 1)."""
     if g is None:
         return None, 1
-    n = 1 if g.dim() == 1 else g.shape[0]
-    if g.dim() > 2 or g.shape[-1] != d or n not in (1, heads) or g.dtype != torch.float32 \
-            or g.device != dev or not g.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous fp32 tensor [1 or {heads}][{d}] on {dev}")
-    return g.data_ptr(), n
+    n = g.shape
+    rows = n[0] if len(n) == 2 else 1
+    if len(n) > 2 or len(n) < 1 or n[-1] != d or (rows != 1 and rows != heads) \
+            or g.dtype is not torch.float32 or g.get_device() != dev or not g.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous fp32 tensor [1 or {heads}][{d}], on the "
+                         "same device")
+    return g.data_ptr(), rows
 
 
 def _first(t, name):
-    """Sizes of the tensor that the others are held against."""
-    if t.dim() != 4 or t.dtype not in _DTYPES:
+    """Sizes, type code and device of the tensor that the others are held against."""
+    n, code = t.shape, _DTYPES.get(t.dtype)
+    if len(n) != 4 or code is None:
         raise ValueError(f"{name}: expected a [B][heads][L][d] tensor of fp32 or bf16")
-    return t.shape[0], t.shape[2], t.shape[3]
+    return n[0], n[2], n[3], t.dtype, code, t.get_device()
 
 
-class _on:
-    """Makes a tensor's device the current one for a call, where it is another."""
+def _bytes(ws, dev):
+    """Pointer and bytes of a workspace tensor."""
+    if ws is None:
+        return None, 0
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("ws: expected a contiguous tensor on the same device")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
-    def __init__(self, dev):
-        self.c = None
-        if dev.type == "cuda" and dev.index != torch.cuda.current_device():
-            self.c = torch.cuda.device(dev)
 
-    def __enter__(self):
-        if self.c is not None:
-            self.c.__enter__()
-
-    def __exit__(self, *e):
-        if self.c is not None:
-            self.c.__exit__(*e)
+def _call(fn, dev, dev_status, stream, *args):
+    """Calls an entry point on the tensors' device and its current (or the given) stream."""
+    if dev < 0:
+        raise ValueError("expected CUDA tensors")
+    if dev_status is not None and (dev_status.get_device() != dev
+                                   or dev_status.dtype is not torch.int32):
+        raise ValueError("dev_status: expected an int32 tensor on the same device")
+    stream = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    if torch._C._cuda_getDevice() == dev:
+        status = fn(*args, _ptr(dev_status), stream)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, _ptr(dev_status), stream)
+    if status != DARK_OK:
+        raise DarkError(status)
 
 
 def dark_rope_init(dims: int, base: float = 10000.0, scale: float = 1.0,
@@ -474,26 +492,23 @@ def dark_qk_norm_rope_fwd(q, k, q_out, k_out, gamma_q=None, gamma_k=None, eps: f
                           dev_status=None, stream=None) -> None:
     """Norms the head rows of q [B][H][L][d] and k [B][Hk][L][d] (k and k_out may be None)
     and rotates them by their positions (int32 [B][L], or None: pos0 + l)."""
-    B, L, d = _first(q, "q")
-    dt, dev = q.dtype, q.device
+    B, L, d, dt, code, dev = _first(q, "q")
     qp, qs, H = _rows(q, "q", B, L, d, dt, dev)
     op, os_, n = _rows(q_out, "q_out", B, L, d, dt, dev)
-    if (k is None) != (k_out is None):
-        raise ValueError("k and k_out: both or neither")
     kp = ks = kop = kos = None
-    Hk = 0
-    if k is not None:
+    Hk = nk = 0
+    if k is not None and k_out is not None:
         kp, ks, Hk = _rows(k, "k", B, L, d, dt, dev)
         kop, kos, nk = _rows(k_out, "k_out", B, L, d, dt, dev)
-    if n != H or (k is not None and nk != Hk):
+    elif k is not k_out:
+        raise ValueError("k and k_out: both or neither")
+    if n != H or nk != Hk:
         raise ValueError("results have other head counts than their inputs")
     gq, hq = _weight(gamma_q, "gamma_q", H, d, dev)
     gk, hk = _weight(gamma_k, "gamma_k", Hk, d, dev)
-    pp = None if positions is None else _want(positions, "positions", (B, L), _INT32, dev)
-    with _on(dev):
-        _check(_lib.dark_qk_norm_rope_fwd(qp, qs, kp, ks, op, os_, kop, kos, gq, hq, gk, hk, eps,
-                                          rope, pp, pos0, B, H, Hk, L, d, _DTYPES[dt],
-                                          _ptr(dev_status), _stream(stream)))
+    _call(_lib.dark_qk_norm_rope_fwd, dev, dev_status, stream, qp, qs, kp, ks, op, os_, kop, kos,
+          gq, hq, gk, hk, eps, rope, _want(positions, "positions", (B, L), torch.int32, dev), pos0,
+          B, H, Hk, L, d, code)
 
 
 def dark_qk_norm_rope_bwd_workspace_bytes(B: int, H: int, Hk: int, L: int, d: int) -> int:
@@ -512,70 +527,51 @@ def dark_qk_norm_rope_bwd(q, k, dq_out, dk_out, dq, dk, gamma_q=None, gamma_k=No
                           dev_status=None, stream=None) -> None:
     """Gradients of dark_qk_norm_rope_fwd: dq, dk of the inputs' type and dgamma_q,
     dgamma_k (fp32, of the weights' shape). ws: see alloc_qk_norm_rope_bwd_workspace."""
-    B, L, d = _first(q, "q")
-    dt, dev = q.dtype, q.device
+    B, L, d, dt, code, dev = _first(q, "q")
     qp, qs, H = _rows(q, "q", B, L, d, dt, dev)
     gp, gs, n1 = _rows(dq_out, "dq_out", B, L, d, dt, dev)
     op, os_, n2 = _rows(dq, "dq", B, L, d, dt, dev)
-    if not (k is None) == (dk_out is None) == (dk is None):
-        raise ValueError("k, dk_out and dk: all or none")
     kp = ks = kgp = kgs = kop = kos = None
     Hk = n3 = n4 = 0
-    if k is not None:
+    if k is not None and dk_out is not None and dk is not None:
         kp, ks, Hk = _rows(k, "k", B, L, d, dt, dev)
         kgp, kgs, n3 = _rows(dk_out, "dk_out", B, L, d, dt, dev)
         kop, kos, n4 = _rows(dk, "dk", B, L, d, dt, dev)
-    if (n1, n2, n3, n4) != (H, H, Hk, Hk):
+    elif k is not None or dk_out is not None or dk is not None:
+        raise ValueError("k, dk_out and dk: all or none")
+    if n1 != H or n2 != H or n3 != Hk or n4 != Hk:
         raise ValueError("gradients have other head counts than their inputs")
     gq, hq = _weight(gamma_q, "gamma_q", H, d, dev)
     gk, hk = _weight(gamma_k, "gamma_k", Hk, d, dev)
     dgq, hdq = _weight(dgamma_q, "dgamma_q", H, d, dev)
     dgk, hdk = _weight(dgamma_k, "dgamma_k", Hk, d, dev)
-    if (gq is not None and dgq is not None and hdq != hq) or \
-            (gk is not None and dgk is not None and hdk != hk):
+    if (gq and dgq and hdq != hq) or (gk and dgk and hdk != hk):
         raise ValueError("a weight's gradient has the weight's shape")
-    pp = None if positions is None else _want(positions, "positions", (B, L), _INT32, dev)
-    with _on(dev):
-        _check(_lib.dark_qk_norm_rope_bwd(qp, qs, kp, ks, gp, gs, kgp, kgs, op, os_, kop, kos, gq,
-                                          hq, gk, hk, dgq, dgk, eps, rope, pp, pos0, B, H, Hk, L,
-                                          d, _DTYPES[dt], *_ws(ws, dev), _ptr(dev_status),
-                                          _stream(stream)))
-
-
-def _ws(ws, dev):
-    """Pointer and bytes of a workspace tensor."""
-    if ws is None:
-        return None, 0
-    if ws.device != dev or not ws.is_contiguous():
-        raise ValueError(f"ws: expected a contiguous tensor on {dev}")
-    return ws.data_ptr(), ws.numel() * ws.element_size()
+    _call(_lib.dark_qk_norm_rope_bwd, dev, dev_status, stream, qp, qs, kp, ks, gp, gs, kgp, kgs,
+          op, os_, kop, kos, gq, hq, gk, hk, dgq, dgk, eps, rope,
+          _want(positions, "positions", (B, L), torch.int32, dev), pos0, B, H, Hk, L, d, code,
+          *_bytes(ws, dev))
 
 
 def kv_cache(k_pages, v_pages) -> dark_kv_cache:
     """The handle of a paged cache: tensors [pages][heads][page_size][d] of keys and values,
-    which have to live as long as it does."""
-    if k_pages.dim() != 4 or k_pages.dtype not in _DTYPES:
+    which it keeps alive."""
+    n, dt, dev = k_pages.shape, k_pages.dtype, k_pages.get_device()
+    if len(n) != 4 or dt not in _DTYPES:
         raise ValueError("k_pages: expected a [pages][heads][page_size][d] tensor of fp32 or bf16")
-    _want(k_pages, "k_pages", k_pages.shape, (k_pages.dtype,), k_pages.device)
-    _want(v_pages, "v_pages", k_pages.shape, (k_pages.dtype,), k_pages.device)
-    c = dark_kv_cache(k_pages.data_ptr(), v_pages.data_ptr(), *k_pages.shape,
-                      _DTYPES[k_pages.dtype])
-    c.tensors = (k_pages, v_pages)
+    c = dark_kv_cache(_want(k_pages, "k_pages", n, dt, dev), _want(v_pages, "v_pages", n, dt, dev),
+                      *n, _DTYPES[dt])
+    c.tensors, c.device = (k_pages, v_pages), dev
     return c
-
-
-def _cache_dtype(cache, t, name):
-    if t.dtype not in _DTYPES or _DTYPES[t.dtype] != cache.dtype:
-        raise ValueError(f"{name}: expected the cache's type")
 
 
 def _lists(page_table, lens, B, dev):
     """A page table [B][max_pages] and lengths [B], int32: pointers and max_pages."""
-    if page_table.dim() != 2:
-        raise ValueError("page_table: expected int32 [B][max_pages]")
-    n = page_table.shape[1]
-    return (_want(page_table, "page_table", (B, n), _INT32, dev), n,
-            _want(lens, "lens", (B,), _INT32, dev))
+    n = page_table.shape
+    if len(n) != 2 or n[0] != B:
+        raise ValueError(f"page_table: expected int32 [{B}][max_pages]")
+    return (_want(page_table, "page_table", n, torch.int32, dev), n[1],
+            _want(lens, "lens", (B,), torch.int32, dev))
 
 
 def dark_kv_append(cache: dark_kv_cache, k, v, page_table, lens, new_lens=None, gamma_k=None,
@@ -584,20 +580,17 @@ def dark_kv_append(cache: dark_kv_cache, k, v, page_table, lens, new_lens=None, 
     """Appends k, v [B][heads][T][d] behind the lens[b] tokens of every sequence, the keys
     normed and rotated on the way. page_table int32 [B][max_pages], lens int32 [B], new_lens
     int32 [B] (None: all T), positions int32 [B][T] (None: pos0 + lens[b] + t)."""
-    B, T, d = _first(k, "k")
-    dt, dev = k.dtype, k.device
-    _cache_dtype(cache, k, "k")
+    B, T, d, dt, code, dev = _first(k, "k")
     kp, ks, n1 = _rows(k, "k", B, T, d, dt, dev)
     vp, vs, n2 = _rows(v, "v", B, T, d, dt, dev)
-    if n1 != cache.heads or n2 != cache.heads or d != cache.d:
-        raise ValueError("k, v: expected the cache's heads and d")
+    if n1 != cache.heads or n2 != n1 or d != cache.d or code != cache.dtype \
+            or cache.device not in (None, dev):
+        raise ValueError("k, v: expected the cache's heads, d, type and device")
     tp, max_pages, lp = _lists(page_table, lens, B, dev)
-    np_ = None if new_lens is None else _want(new_lens, "new_lens", (B,), _INT32, dev)
-    pp = None if positions is None else _want(positions, "positions", (B, T), _INT32, dev)
     g, hg = _weight(gamma_k, "gamma_k", n1, d, dev)
-    with _on(dev):
-        _check(_lib.dark_kv_append(cache, kp, ks, vp, vs, B, T, tp, max_pages, lp, np_, g, hg, eps,
-                                   rope, pp, pos0, _ptr(dev_status), _stream(stream)))
+    _call(_lib.dark_kv_append, dev, dev_status, stream, cache, kp, ks, vp, vs, B, T, tp, max_pages,
+          lp, _want(new_lens, "new_lens", (B,), torch.int32, dev), g, hg, eps, rope,
+          _want(positions, "positions", (B, T), torch.int32, dev), pos0)
 
 
 def dark_cache_attention_workspace_bytes(proj: dark_projection, cache: dark_kv_cache, B: int,
@@ -618,23 +611,21 @@ def dark_cache_attention_fwd(proj: dark_projection, cache: dark_kv_cache, q, out
     """Exact-mode attention of q [B][H][T][d] over the shared prefix (prefix_pages int32
     [ceil(prefix_len / page_size)]) and each sequence's lens[b] own tokens. ws: see
     alloc_cache_attention_workspace."""
-    B, T, d = _first(q, "q")
-    dt, dev = q.dtype, q.device
-    _cache_dtype(cache, q, "q")
+    B, T, d, dt, code, dev = _first(q, "q")
     qp, qs, H = _rows(q, "q", B, T, d, dt, dev)
     op, os_, n = _rows(out, "out", B, T, d, dt, dev)
-    if n != H or d != cache.d:
-        raise ValueError("q, out: expected equal head counts and the cache's d")
+    if n != H or d != cache.d or code != cache.dtype \
+            or cache.device not in (None, dev):
+        raise ValueError("q, out: expected equal head counts and the cache's d, type and device")
     tp, max_pages, lp = _lists(page_table, lens, B, dev)
     xp = None
     if prefix_len > 0 and prefix_pages is not None:
-        if prefix_pages.dim() != 1 or prefix_pages.shape[0] * cache.page_size < prefix_len:
+        n = prefix_pages.shape
+        if len(n) != 1 or n[0] * cache.page_size < prefix_len:
             raise ValueError("prefix_pages: expected int32 [ceil(prefix_len / page_size)]")
-        xp = _want(prefix_pages, "prefix_pages", prefix_pages.shape, _INT32, dev)
-    with _on(dev):
-        _check(_lib.dark_cache_attention_fwd(proj, cache, qp, qs, op, os_, B, H, T, xp, prefix_len,
-                                             tp, max_pages, lp, flags, *_ws(ws, dev),
-                                             _ptr(dev_status), _stream(stream)))
+        xp = _want(prefix_pages, "prefix_pages", n, torch.int32, dev)
+    _call(_lib.dark_cache_attention_fwd, dev, dev_status, stream, proj, cache, qp, qs, op, os_, B,
+          H, T, xp, prefix_len, tp, max_pages, lp, flags, *_bytes(ws, dev))
 
 
 class RedrawSchedule:
