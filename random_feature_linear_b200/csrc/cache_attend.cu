@@ -379,6 +379,22 @@ int row_block(const Plan& p, int rows) {
   return rows >= 32 ? 32 : 8;
 }
 
+// Ranges of the tcgen05 kernel (one CTA an SM): the count whose waves of CTAs, each with
+// its tiles and about two tiles' time to start and end, take the least time.
+void split_tiles(const CacheAttnArgs& a, Plan* p) {
+  const long long tiles = (a.prefix_len + kTcKeys - 1) / kTcKeys;
+  const long long blocks = (long long)a.Hk * ((p->all + tc_rows(p->dp) - 1) / tc_rows(p->dp));
+  long long best = -1;
+  for (long long s = 1; s <= tiles && (s == 1 || blocks * s <= 4 * 148); ++s) {
+    const long long per = (tiles + s - 1) / s, cost = (blocks * s + 147) / 148 * (per + 2);
+    if (best < 0 || cost < best) {
+      best = cost;
+      p->p_chunk = (int)(per * kTcKeys);
+    }
+  }
+  p->p_splits = (a.prefix_len + p->p_chunk - 1) / p->p_chunk;
+}
+
 Plan make_plan(const CacheAttnArgs& a) {
   Plan p;
   memset(&p, 0, sizeof(p));
@@ -386,6 +402,7 @@ Plan make_plan(const CacheAttnArgs& a) {
   p.all = a.B * p.rows;
   p.mma = a.dtype == DARK_BF16 && a.d % 8 == 0;
   p.dp = p.mma ? (a.d <= 64 ? 64 : a.d <= 128 ? 128 : 256) : a.d;
+  p.tc = p.mma && p.all >= 64 && a.prefix_len >= 256;
   // ranges: about four CTAs an SM over key heads, row blocks and ranges
   const long long want = 4LL * 148;
   const long long pb = (long long)a.Hk * ((p.all + row_block(p, p.all) - 1) / row_block(p, p.all));
@@ -395,6 +412,7 @@ Plan make_plan(const CacheAttnArgs& a) {
   if (s < 1) s = 1;
   p.p_chunk = steps == 0 ? kKeyStep : (int)((steps + s - 1) / s * kKeyStep);
   p.p_splits = steps == 0 ? 1 : (a.prefix_len + p.p_chunk - 1) / p.p_chunk;
+  if (p.tc) split_tiles(a, &p);
   const long long ob = (long long)a.Hk * ((p.rows + row_block(p, p.rows) - 1) / row_block(p, p.rows));
   p.cap = a.B + (int)((want + ob - 1) / ob);
   size_t o = kWsHeader;
@@ -435,6 +453,10 @@ cudaError_t launch_all(const Params& q) {
   queries_kernel<T><<<dim3((n + kPrepRows - 1) / kPrepRows + 1, q.a.H), 256, smem, q.a.stream>>>(q);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
+  if (q.p.tc) {
+    e = launch_prefix_tc(q);
+    if (e != cudaSuccess) return e;
+  }
   if (q.p.mma) {
     e = launch_ranges_mma(q);
     if (e != cudaSuccess) return e;
@@ -460,6 +482,7 @@ cudaError_t launch_cache_attention(const CacheAttnArgs& a) {
   q.a = a;
   q.p = cache::make_plan(a);
   q.G = a.H / a.Hk;
+  q.stall = test_stall_cycles();
   return a.dtype == DARK_BF16 ? cache::launch_all<__nv_bfloat16>(q) : cache::launch_all<float>(q);
 }
 

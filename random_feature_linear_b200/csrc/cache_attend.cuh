@@ -22,6 +22,7 @@ struct Plan {
   int rows, all;                          // G T rows of a sequence, B G T rows of a key head
   int dp;                                 // columns of the stored queries (d, padded)
   int mma;                                // bf16 with 16-byte rows: tensor cores
+  int tc;                                 // the prefix by 128-row tiles (tcgen05)
   int p_splits, p_chunk;                  // ranges of the prefix, keys of a range
   int cap;                                // own ranges of all sequences, at most
   // byte offsets into the workspace
@@ -39,6 +40,7 @@ struct Params {
   CacheAttnArgs a;
   Plan p;
   int G;
+  long long stall;                        // testing stall of the tcgen05 kernel (0: none)
 };
 
 __host__ __device__ inline int* sched_off(Sched* s) { return reinterpret_cast<int*>(s + 1); }

@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kWarps * 32) range_mma_kernel(const __grid_con
   constexpr int NS = DP / 16, NT = DP / 8;                // k-steps of a score, column tiles
   constexpr int RB = 8 * RT, S = C::kStages;
   const int hk = blockIdx.y;
-  const Item it = item_of(q, blockIdx.x, hk, RB, q.a.prefix_len > 0, true);
+  const Item it = item_of(q, blockIdx.x, hk, RB, q.a.prefix_len > 0 && !q.p.tc, true);
   if (!it.any) return;
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -340,7 +340,7 @@ cudaError_t launch(const Params& q, long long n) {
 cudaError_t launch_ranges_mma(const Params& q) {
   const int dp = q.p.dp, rb = mma_rows(dp, q.p.rows);
   long long n = (long long)q.p.cap * ((q.p.rows + rb - 1) / rb);
-  if (q.a.prefix_len > 0) n += (long long)q.p.p_splits * ((q.p.all + rb - 1) / rb);
+  if (q.a.prefix_len > 0 && !q.p.tc) n += (long long)q.p.p_splits * ((q.p.all + rb - 1) / rb);
   if (dp == 256) return launch<256, 1>(q, n);
   if (dp == 128) return rb == 8 ? launch<128, 1>(q, n) : launch<128, 2>(q, n);
   return rb == 8 ? launch<64, 1>(q, n) : launch<64, 2>(q, n);

@@ -10,6 +10,11 @@ namespace cache {
 inline int mma_rows(int dp, int rows) { return dp <= 128 && rows > 8 ? 16 : 8; }
 cudaError_t launch_ranges_mma(const Params& q);
 
+// Rows of a tile block of the tcgen05 kernel, keys of its tiles.
+inline int tc_rows(int dp) { return dp == 256 ? 128 : 256; }
+constexpr int kTcKeys = 128;
+cudaError_t launch_prefix_tc(const Params& q);
+
 // Queries for the tensor cores: y = hi + lo in bf16 (16 bits of significand together;
 // one bf16 alone would move the exponents by 2^-9 relative, as much again as the rounding
 // of the output). hi rows first, then all lo rows, dp columns each.

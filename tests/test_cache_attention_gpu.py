@@ -184,6 +184,14 @@ CASES = {
                                 lens=tuple(range(3, 43))),
     "many-rows-d80": dict(B=50, H=4, Hk=1, T=1, d=80, r=80, page=24, prefix=421,
                           lens=tuple(range(50))),
+    "many-rows-d256": dict(B=20, H=8, Hk=2, T=2, d=256, r=64, page=48, prefix=700,
+                           lens=tuple(range(0, 60, 3))),
+    "many-rows-d40": dict(B=30, H=4, Hk=1, T=2, d=40, r=40, page=24, prefix=300,
+                          lens=tuple(range(30))),
+    "many-rows-large-scores": dict(B=20, H=8, Hk=1, T=2, d=64, page=16, prefix=1300,
+                                   q_scale=12.0, lens=tuple(range(2, 102, 5))),
+    "many-rows-page-of-one": dict(B=17, H=4, Hk=1, page=1, d=128, r=64, prefix=300,
+                                  lens=tuple(range(17))),
     "fp32": dict(dtype=F, B=3, H=6, Hk=2, T=3, d=40, r=24, page=24, prefix=100, lens=(77, 3, 30),
                  causal=True),
     "fp32-many-rows": dict(dtype=F, B=10, H=8, Hk=2, T=2, d=64, page=16, prefix=200,
@@ -224,6 +232,32 @@ def test_a_large_score_selects_its_key(D, cuda_ok, dtype, B):
     c.run()
     # the others' weight is below 140 e^-40; the value itself is rounded once more
     torch.testing.assert_close(c.out, want, rtol=2.0 ** -7, atol=1e-4)
+
+
+@pytest.mark.parametrize("d,page", [(64, 64), (128, 24), (256, 128)])
+def test_long_prefix(D, cuda_ok, d, page):
+    """Many tiles a range: against fp64 products on the GPU, root mean square error. The
+    roundings of the query, the weights and the result are each at most 2^-8 relative and
+    independent: together below sqrt(3) 2^-8 of the root mean square output, with the
+    queries' and weights' part growing no faster than the output's own sum."""
+    B, H, T, prefix = 64, 8, 8, 20011
+    c = Call(D, B=B, H=H, Hk=1, T=T, d=d, r=d, page=page, prefix=prefix, lens=(9,) * B, causal=True)
+    c.run()
+    assert c.status.item() == 0
+    k, v = (x[c.d_shared.long()].double().permute(1, 0, 2, 3).reshape(-1, d)[:prefix]
+            for x in (c.kp, c.vp))
+    m = torch.from_numpy(c.stored_geom()).cuda()
+    for b in range(0, B, 13):
+        own = c.d_table[b].long()
+        kk, vv = (torch.cat([p, x[own].double().permute(1, 0, 2, 3).reshape(-1, d)[:9]])
+                  for p, x in ((k, c.kp), (v, c.vp)))
+        y = torch.einsum("hri,hrj,hti->htj", m, m, c.q[b].double()) / d ** 0.5
+        z = y @ kk.T
+        last = prefix + 9 - T + torch.arange(T, device="cuda")
+        z = z.where(torch.arange(len(kk), device="cuda") <= last[:, None], -torch.inf)
+        ref = torch.softmax(z, dim=-1) @ vv
+        err = (c.out[b].double() - ref).pow(2).mean().sqrt() / ref.pow(2).mean().sqrt()
+        assert err <= 3 ** 0.5 * H8
 
 
 @pytest.mark.parametrize("dtype,d", [(BF, 64), (BF, 256), (BF, 36), (F, 64)])
@@ -370,3 +404,19 @@ def test_decoding_with_the_cache_is_causal_attention(D, cuda_ok, dtype):
         assert (err.max(axis=(2, 3)) / np.abs(want).max(axis=(2, 3))).max() <= 1e-4
     else:
         assert err.max() <= 2e-2
+
+
+def test_a_wait_that_runs_out_is_reported(D, cuda_ok):
+    """The tcgen05 kernel's waits are bounded: the testing stall ends in a status, and the
+    next call is right again."""
+    c = Call(D, B=20, H=8, Hk=1, T=2, prefix=600, lens=tuple(range(2, 42, 2)))
+    D.dark_set_test_stall_cycles(20000)
+    try:
+        c.run()
+        torch.cuda.synchronize()
+    finally:
+        D.dark_set_test_stall_cycles(0)
+    assert c.status.item() == D.DARK_ERR_TIMEOUT
+    c.status.zero_()
+    c.run()
+    c.check()
