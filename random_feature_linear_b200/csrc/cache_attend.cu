@@ -16,9 +16,8 @@
 #include <math.h>
 #include <string.h>
 
-#include "cache_attend.cuh"
 #include "cache_attend_mma.cuh"
-#include "tc_common.cuh"
+#include "cache_sched.cuh"
 
 namespace dark {
 namespace cache {
@@ -26,69 +25,7 @@ namespace {
 
 constexpr int kPrepRows = 8;
 
-// ------------------------------------------------- queries and the cut of keys --
-
-// The cut of the own keys: ranges of `chunk` keys, as short as `cap` ranges allow (so
-// that a few long sequences spread over the GPU too).
-__device__ void make_sched(const Params& q) {
-  __shared__ int part[33];
-  __shared__ long long wsum[32];
-  __shared__ int chunk_s;
-  Sched* sc = at<Sched>(q.a, q.p.o_sched);
-  int* off = sched_off(sc);
-  int* len = sched_len(sc, q.a.B);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x / 32;
-  const int64_t most = (int64_t)q.a.max_pages * q.a.page;
-  long long sum = 0;
-  for (int b = tid; b < q.a.B; b += blockDim.x) {
-    int64_t n = q.a.lens[b];
-    if (n < 0 || n > most) {
-      report(q.a.dev_status, DARK_ERR_INVALID_ARG);
-      n = n < 0 ? 0 : most;
-    }
-    len[b] = (int)n;
-    sum += n;
-  }
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) wsum[warp] = sum;
-  __syncthreads();
-  if (tid == 0) {
-    long long all = 0;
-    for (int w = 0; w < nw; ++w) all += wsum[w];
-    // sum ceil(len / chunk) <= all / chunk + B <= cap
-    const long long room = q.p.cap - q.a.B > 0 ? q.p.cap - q.a.B : 1;
-    long long c = (all + room - 1) / room;
-    c = (c + kKeyStep - 1) / kKeyStep * kKeyStep;
-    // no sequence is longer than 2^30 keys: longer ranges change nothing
-    chunk_s = c < 2 * kKeyStep ? 2 * kKeyStep : c < (1 << 30) ? (int)c : 1 << 30;
-  }
-  __syncthreads();
-  const int chunk = chunk_s;
-  int base = 0;
-  for (int b0 = 0; b0 < q.a.B; b0 += blockDim.x) {
-    const int b = b0 + tid;
-    const int n = b < q.a.B ? (int)(((long long)len[b] + chunk - 1) / chunk) : 0;
-    int x = n;
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane == 31) part[warp] = x;
-    __syncthreads();
-    int before = base;
-    for (int w = 0; w < warp; ++w) before += part[w];
-    if (b < q.a.B) off[b] = before + x - n;
-    int all = 0;
-    for (int w = 0; w < nw; ++w) all += part[w];
-    base += all;
-    __syncthreads();
-  }
-  if (tid == 0) {
-    off[q.a.B] = base;
-    sc->chunk = chunk;
-    sc->total = base;
-  }
-}
+// --------------------------------------------------- queries in fp32 (SIMT) --
 
 // y of kPrepRows rows of one query head: p = (c_m M) q, y = 2 (c_m M)^T p. Threads over
 // the rows of M, then over the columns; sums in fp32.
@@ -143,10 +80,7 @@ __global__ void __launch_bounds__(256) queries_kernel(const __grid_constant__ Pa
     for (int k = 0; k < kPrepRows && n0 + k < n; ++k) {
       const int b = (n0 + k) / q.a.T, t = (n0 + k) - b * q.a.T;
       const int64_t row = (int64_t)hk * q.p.all + (b * q.G + g) * q.a.T + t;
-      if (q.p.mma)
-        store_query_hi_lo(at<__nv_bfloat16>(q.a, q.p.o_y), (int64_t)q.a.Hk * q.p.all, row, dp, c, s[k]);
-      else
-        at<float>(q.a, q.p.o_y)[row * dp + c] = s[k];
+      at<float>(q.a, q.p.o_y)[row * dp + c] = s[k];
     }
   }
 }
@@ -323,51 +257,81 @@ __global__ void __launch_bounds__(128) range_kernel(const __grid_constant__ Para
 // -------------------------------------------------------------------- the join --
 
 // One warp a row: out = sum_i 2^(m_i - m) acc_i / sum_i 2^(m_i - m) l_i over the row's
-// prefix and own ranges, in their order. Rows that see no key give zeros.
+// prefix and own ranges, in their order. Rows that see no key give zeros. Lanes take the
+// ranges' exponents and weights 32 at a time, then float4 columns of 32 / lanes_of_d ranges
+// at once, so that the ranges' sums load without waiting for one another.
 template <typename T>
 __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Params q) {
+  pdl_wait();
   const int lane = threadIdx.x & 31;
   const int64_t n = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
   if (n >= (int64_t)q.a.Hk * q.p.all) return;
   const int hk = (int)(n / q.p.all), row = (int)(n - (int64_t)hk * q.p.all);
   const int b = row / q.p.rows, in = row - b * q.p.rows, g = in / q.a.T, t = in - g * q.a.T;
-  Sched* sc = at<Sched>(q.a, q.p.o_sched);
-  const int len = sched_len(sc, q.a.B)[b], r0 = sched_off(sc)[b], r1 = sched_off(sc)[b + 1];
+  const int len = sched_len(q)[b], r0 = sched_off(q)[b], r1 = sched_off(q)[b + 1];
   const bool pad = (q.a.flags & DARK_CAUSAL) && len - q.a.T + t < 0;
   const int d = q.a.d, np = q.a.prefix_len > 0 && !pad ? q.p.p_splits : 0, no = pad ? 0 : r1 - r0;
-  const float* pml = at<float>(q.a, q.p.o_pml) + ((size_t)hk * q.p.p_splits * q.p.all + row) * 2;
-  const float* oml = at<float>(q.a, q.p.o_oml) + (((size_t)hk * q.p.cap + r0) * q.p.rows + in) * 2;
+  const int total = np + no;
+  const int64_t pslot = (int64_t)hk * q.p.p_splits * q.p.all + row, pstep = q.p.all;
+  const int64_t oslot = ((int64_t)hk * q.p.cap + r0) * q.p.rows + in, ostep = q.p.rows;
+  const float2* pml = at<float2>(q.a, q.p.o_pml) + pslot;
+  const float2* oml = at<float2>(q.a, q.p.o_oml) + oslot;
   auto ml = [&](int i) {
-    return *reinterpret_cast<const float2*>(i < np ? pml + (size_t)i * q.p.all * 2
-                                                   : oml + (size_t)(i - np) * q.p.rows * 2);
+    return i >= total ? make_float2(-INFINITY, 0.f) : i < np ? pml[i * pstep] : oml[(i - np) * ostep];
   };
-  float top = -INFINITY;
-  for (int i = lane; i < np + no; i += 32) top = fmaxf(top, ml(i).x);
+  // columns: `per` lanes a range (8, 16 or 32), float4 c, c + 128
+  const int per = d <= 32 ? 8 : d <= 64 ? 16 : 32, sub = lane / per, subs = 32 / per;
+  const int c = 4 * (lane % per);
+  const float* pa = at<float>(q.a, q.p.o_pacc) + pslot * d;
+  const float* oa = at<float>(q.a, q.p.o_oacc) + oslot * d;
+  float2 mine = ml(lane);
+  float top = mine.x;
+  for (int i = lane + 32; i < total; i += 32) top = fmaxf(top, ml(i).x);
   top = warp_max(top);
   const float ref = top == -INFINITY ? 0.f : top;
-  const float* pa = at<float>(q.a, q.p.o_pacc) + ((size_t)hk * q.p.p_splits * q.p.all + row) * d;
-  const float* oa = at<float>(q.a, q.p.o_oacc) + (((size_t)hk * q.p.cap + r0) * q.p.rows + in) * d;
-  float l = 0.f, o[8];
+  float l = 0.f;
+  float4 o[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+  for (int i0 = 0; i0 < total; i0 += 32) {
+    if (i0 > 0) mine = ml(i0 + lane);
+    const float f = exp2f(mine.x - ref);
+    l += f * mine.y;
+    const int count = min(32, total - i0);
+#pragma unroll 4
+    for (int i = 0; i < count; i += subs) {
+      const int k = i0 + i + sub;
+      const float w = __shfl_sync(0xffffffffu, f, i + sub);
+      if (w == 0.f || k >= total) continue;            // no visible key: acc is not read
+      const float* src = k < np ? pa + k * pstep * d : oa + (k - np) * ostep * d;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) o[j] = 0.f;
-  for (int i = 0; i < np + no; ++i) {
-    const float2 v = ml(i);
-    const float f = exp2f(v.x - ref);
-    l = fmaf(f, v.y, l);
-    if (f == 0.f) continue;                            // no visible key: acc is not read
-    const float* src = i < np ? pa + (size_t)i * q.p.all * d : oa + (size_t)(i - np) * q.p.rows * d;
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (lane + 32 * j < d) o[j] = fmaf(f, src[lane + 32 * j], o[j]);
+      for (int j = 0; j < 2; ++j) {
+        if (c + 128 * j >= d) break;
+        const float4 v = *reinterpret_cast<const float4*>(src + c + 128 * j);
+        o[j].x = fmaf(w, v.x, o[j].x);
+        o[j].y = fmaf(w, v.y, o[j].y);
+        o[j].z = fmaf(w, v.z, o[j].z);
+        o[j].w = fmaf(w, v.w, o[j].w);
+      }
+    }
+  }
+  l = warp_sum(l);
+  for (int s = per; s < 32; s <<= 1) {
+    o[0].x += __shfl_xor_sync(0xffffffffu, o[0].x, s);
+    o[0].y += __shfl_xor_sync(0xffffffffu, o[0].y, s);
+    o[0].z += __shfl_xor_sync(0xffffffffu, o[0].z, s);
+    o[0].w += __shfl_xor_sync(0xffffffffu, o[0].w, s);
   }
   T* dst = (T*)q.a.out + b * q.a.os[0] + (int64_t)(hk * q.G + g) * q.a.os[1] + t * q.a.os[2];
   bool bad = false;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    if (lane + 32 * j >= d) continue;
-    const float v = l == 0.f ? 0.f : o[j] / l;
-    bad |= !isfinite(v);
-    dst[lane + 32 * j] = from_f32<T>(v);
+  for (int j = 0; j < 2; ++j) {
+    const float v[4] = {o[j].x, o[j].y, o[j].z, o[j].w};
+    if (sub > 0 || c + 128 * j >= d) break;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float x = l == 0.f ? 0.f : v[e] / l;
+      bad |= !isfinite(x);
+      dst[c + 128 * j + e] = from_f32<T>(x);
+    }
   }
   if (bad) report(q.a.dev_status, DARK_ERR_NUMERIC);
 }
@@ -422,7 +386,7 @@ Plan make_plan(const CacheAttnArgs& a) {
     return at;
   };
   const size_t krows = (size_t)a.Hk * p.all;
-  p.o_sched = take(sizeof(Sched) + (size_t)(2 * a.B + 1) * 4);
+  p.o_sched = take((size_t)p.cap * 16 + (size_t)(2 * a.B + 1) * 4);
   p.o_y = take(krows * p.dp * 4);
   p.o_pacc = take(a.prefix_len > 0 ? krows * p.p_splits * a.d * 4 : 0);
   p.o_pml = take(a.prefix_len > 0 ? krows * p.p_splits * 8 : 0);
@@ -449,16 +413,18 @@ cudaError_t launch_range(const Params& q, bool prefix) {
 template <typename T>
 cudaError_t launch_all(const Params& q) {
   const int n = q.a.B * q.a.T;
-  const size_t smem = (size_t)kPrepRows * (q.a.d + q.a.r) * 4;
-  queries_kernel<T><<<dim3((n + kPrepRows - 1) / kPrepRows + 1, q.a.H), 256, smem, q.a.stream>>>(q);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  if (q.p.tc) {
-    e = launch_prefix_tc(q);
-    if (e != cudaSuccess) return e;
-  }
+  cudaError_t e;
   if (q.p.mma) {
-    e = launch_ranges_mma(q);
+    e = launch_queries_mma(q);
+  } else {
+    const size_t smem = (size_t)kPrepRows * (q.a.d + q.a.r) * 4;
+    queries_kernel<T><<<dim3((n + kPrepRows - 1) / kPrepRows + 1, q.a.H), 256, smem, q.a.stream>>>(q);
+    e = cudaGetLastError();
+  }
+  if (e != cudaSuccess) return e;
+  if (q.p.mma) {
+    if (q.p.tc) e = launch_prefix_tc(q);
+    if (e == cudaSuccess) e = launch_ranges_mma(q);
     if (e != cudaSuccess) return e;
   } else {
     for (int prefix = q.a.prefix_len > 0 ? 1 : 0; prefix >= 0; --prefix) {
@@ -468,8 +434,7 @@ cudaError_t launch_all(const Params& q) {
     }
   }
   const int64_t rows = (int64_t)q.a.Hk * q.p.all;
-  join_kernel<T><<<(unsigned)((rows + 3) / 4), 128, 0, q.a.stream>>>(q);
-  return cudaGetLastError();
+  return launch_dependent(join_kernel<T>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, q.a.stream, q);
 }
 
 }  // namespace

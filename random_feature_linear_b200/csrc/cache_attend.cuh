@@ -29,13 +29,9 @@ struct Plan {
   size_t o_sched, o_y, o_pacc, o_pml, o_oacc, o_oml, bytes;
 };
 
-// Written on the device from the sequences' lengths (one block of the first launch).
-struct Sched {
-  int chunk;                              // keys of an own range
-  int total;                              // own ranges of all sequences
-  // followed by int off[B + 1] (ranges before sequence b) and int len[B]
-};
-
+// The cut of the own keys, written on the device from the sequences' lengths (one block
+// of the first launch): int4 range[cap] = (sequence, first key, end, length), empty ones
+// (0, 0, 0, 0) behind the last, then int off[B + 1] (ranges before sequence b), int len[B].
 struct Params {
   CacheAttnArgs a;
   Plan p;
@@ -43,13 +39,16 @@ struct Params {
   long long stall;                        // testing stall of the tcgen05 kernel (0: none)
 };
 
-__host__ __device__ inline int* sched_off(Sched* s) { return reinterpret_cast<int*>(s + 1); }
-__host__ __device__ inline int* sched_len(Sched* s, int B) { return sched_off(s) + B + 1; }
-
 template <typename T>
 __host__ __device__ inline T* at(const CacheAttnArgs& a, size_t off) {
   return reinterpret_cast<T*>(reinterpret_cast<char*>(a.ws) + off);
 }
+
+__device__ inline int4* sched_range(const Params& q) { return at<int4>(q.a, q.p.o_sched); }
+__device__ inline int* sched_off(const Params& q) {
+  return reinterpret_cast<int*>(sched_range(q) + q.p.cap);
+}
+__device__ inline int* sched_len(const Params& q) { return sched_off(q) + q.a.B + 1; }
 
 // One CTA's work: keys [k0, k1) of a page list, rows [row0, row0 + nrows) of a key head.
 struct Item {
@@ -89,21 +88,13 @@ __device__ __forceinline__ Item item_of(const Params& q, int x, int hk, int rb, 
   if (!own) return it;
   const int nb = (p.rows + rb - 1) / rb;
   const int r = x / nb, blk = x % nb;
-  Sched* sc = at<Sched>(q.a, p.o_sched);
-  if (r >= sc->total) return it;
-  const int* off = sched_off(sc);
-  int lo = 0, hi = q.a.B;                 // the last b with off[b] <= r
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (off[mid] <= r) lo = mid; else hi = mid;
-  }
-  const int len = sched_len(sc, q.a.B)[lo];
-  it.pages = q.a.table + (int64_t)lo * q.a.max_pages;
-  it.k0 = (r - off[lo]) * sc->chunk;
-  it.k1 = it.k0 + sc->chunk < len ? it.k0 + sc->chunk : len;
-  it.row0 = lo * p.rows + blk * rb;
+  const int4 v = sched_range(q)[r];
+  it.pages = q.a.table + (int64_t)v.x * q.a.max_pages;
+  it.k0 = v.y;
+  it.k1 = v.z;
+  it.row0 = v.x * p.rows + blk * rb;
   it.nrows = p.rows - blk * rb < rb ? p.rows - blk * rb : rb;
-  it.len = len;
+  it.len = v.w;
   const size_t slot = ((size_t)hk * p.cap + r) * p.rows + blk * rb;
   it.acc = at<float>(q.a, p.o_oacc) + slot * q.a.d;
   it.ml = at<float>(q.a, p.o_oml) + slot * 2;

@@ -24,43 +24,6 @@ namespace {
 
 constexpr int kWarps = 4, kKeys = 16;
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// Byte offset of 16-byte chunk `c` of row `row` in a tile of DP bf16 columns: chunks
-// XORed with the row's low bits, so that eight rows at one chunk hit eight bank groups.
-template <int DP>
-__device__ __forceinline__ uint32_t tile_off(int row, int c) {
-  return (uint32_t)(row * DP * 2 + ((c ^ (row & 7)) << 4));
-}
-
 __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
@@ -96,6 +59,8 @@ __global__ void __launch_bounds__(kWarps * 32) range_mma_kernel(const __grid_con
   constexpr int NS = DP / 16, NT = DP / 8;                // k-steps of a score, column tiles
   constexpr int RB = 8 * RT, S = C::kStages;
   const int hk = blockIdx.y;
+  pdl_wait();
+  pdl_launch();
   const Item it = item_of(q, blockIdx.x, hk, RB, q.a.prefix_len > 0 && !q.p.tc, true);
   if (!it.any) return;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -197,8 +162,8 @@ __global__ void __launch_bounds__(kWarps * 32) range_mma_kernel(const __grid_con
       ldsm4(b, k0 + tile_off<DP>((lg >> 1) * 8 + lr, 2 * st + (lg & 1)));
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
-        mma16816(s[rt][0], ya[rt][st], b[0], b[1]);
-        mma16816(s[rt][1], ya[rt][st], b[2], b[3]);
+        mma16816_bf16(s[rt][0], ya[rt][st], b[0], b[1]);
+        mma16816_bf16(s[rt][1], ya[rt][st], b[2], b[3]);
       }
     }
     const int key0 = it.k0 + (warp + i * kWarps) * kKeys + 2 * t;
@@ -270,8 +235,8 @@ __global__ void __launch_bounds__(kWarps * 32) range_mma_kernel(const __grid_con
       ldsm4_t(b, v0 + tile_off<DP>((lg & 1) * 8 + lr, n + (lg >> 1)));
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
-        mma16816(o[rt][n], pa[rt], b[0], b[1]);
-        mma16816(o[rt][n + 1], pa[rt], b[2], b[3]);
+        mma16816_bf16(o[rt][n], pa[rt], b[0], b[1]);
+        mma16816_bf16(o[rt][n + 1], pa[rt], b[2], b[3]);
       }
     }
     __syncwarp();                                         // the slot may be filled again
@@ -331,8 +296,8 @@ cudaError_t launch(const Params& q, long long n) {
   static int smem_set[64];
   cudaError_t e = set_smem_limit_once((const void*)range_mma_kernel<DP, RT>, (int)C::kSmem, smem_set);
   if (e != cudaSuccess) return e;
-  range_mma_kernel<DP, RT><<<dim3((unsigned)n, q.a.Hk), kWarps * 32, C::kSmem, q.a.stream>>>(q);
-  return cudaGetLastError();
+  return launch_dependent(range_mma_kernel<DP, RT>, dim3((unsigned)n, q.a.Hk), dim3(kWarps * 32),
+                          C::kSmem, q.a.stream, q);
 }
 
 }  // namespace

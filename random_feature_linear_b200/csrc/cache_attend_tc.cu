@@ -65,16 +65,6 @@ __device__ __forceinline__ void tmem_st16_async(uint32_t taddr, const uint32_t (
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // Whether any of the 128 loading threads passes `bad`.
 __device__ __forceinline__ bool loaders_sync_or(bool bad) {
   uint32_t r;
@@ -89,6 +79,19 @@ __device__ __forceinline__ bool loaders_sync_or(bool bad) {
   return r != 0;
 }
 
+// Whether the phase with the given parity has completed (does not wait).
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 struct Bars {
   uint64_t q, never, drain;
   uint64_t s[2], p[2], o[2];              // per row tile: scores, weights, sums are ready
@@ -101,6 +104,7 @@ template <int DP>
 __global__ void __launch_bounds__(kThreads, 1) range_tc_kernel(const __grid_constant__ Params q) {
   using C = Tc<DP>;
   constexpr int RT = C::RT, S = C::kSlots, CH = DP / 8;
+  static_assert(S >= 2 && S <= 8, "ring");
   static_assert(sizeof(Bars) <= 256, "barriers");
   const int hk = blockIdx.y;
   const Item it = item_of(q, blockIdx.x, hk, RT * kT, true, false);
@@ -137,6 +141,8 @@ __global__ void __launch_bounds__(kThreads, 1) range_tc_kernel(const __grid_cons
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bar->tmem;
+  pdl_wait();
+  pdl_launch();
   bool go = true;
   if (q.stall > 0) {
     if (tid == 0) wait_one(&bar->never, 0, abort, status, q.stall);
@@ -145,10 +151,9 @@ __global__ void __launch_bounds__(kThreads, 1) range_tc_kernel(const __grid_cons
   }
 
   if (go && warp >= 8 && warp < 12) {
-    // ---- queries, then tiles K_0, V_0, K_1, V_1, ... through the ring. A slot is handed
-    // over LAG copies later, when this thread's part of it has arrived. The threads agree
-    // on an abort before each key tile (they share the tile's row numbers).
-    constexpr int LAG = S >= 4 ? 2 : 1;
+    // ---- queries, then tiles K_0, V_0, K_1, V_1, ... through the ring; a copy is handed
+    // over when this thread's part of it has arrived. The threads agree on an abort before
+    // each key tile (they share the tile's row numbers).
     const int t = tid - 256, c = t % CH;
     const __nv_bfloat16* y = at<__nv_bfloat16>(q.a, q.p.o_y) + ((int64_t)hk * q.p.all + it.row0) * DP;
     for (int r = t / CH; r < rts * kT; r += kT / CH)
@@ -157,46 +162,58 @@ __global__ void __launch_bounds__(kThreads, 1) range_tc_kernel(const __grid_cons
     cp_commit();
     int64_t* rows = reinterpret_cast<int64_t*>(sm + C::oRows);
     const bool in = c < 2 * ks, has = c * 8 < d;      // (a last half step is zeros)
-    bool ok = true;
     const int n = 2 * tiles;
-    for (int i = 0; i < n + LAG; ++i) {
-      if (i < n) {
-        const int slot = i % S, j = i / 2;
-        if (ok && i >= S) ok = wait_one(&bar->empty[slot], (i / S - 1) & 1, abort, status);
-        if (!(i & 1)) {                               // rows of the tile's keys, one a thread
-          const int key = it.k0 + j * kT + t;
-          int64_t row = -1;
-          if (key < it.k1) {
-            row = cache_row(q.a, it.pages, key, hk);
-            if (row < 0) report(status, DARK_ERR_INVALID_ARG);
-          }
-          rows[(j & 1) * kT + t] = row;
-          ok = !loaders_sync_or(!ok);
-          if (!ok) break;
-        }
-        if (ok && in) {
-          const __nv_bfloat16* pool = (const __nv_bfloat16*)(i & 1 ? q.a.vp : q.a.kp) + c * 8;
-          const uint32_t dst = s0 + C::oRing + slot * C::kTile;
+    // row of the cache that this thread looks up for tile j; the page a tile ahead of its use
+    auto lookup = [&](int j) {
+      const int key = it.k0 + j * kT + t;
+      if (key >= it.k1) return (int64_t)-1;
+      const int64_t row = cache_row(q.a, it.pages, key, hk);
+      if (row < 0) report(status, DARK_ERR_INVALID_ARG);
+      return row;
+    };
+    int64_t next_row = lookup(0);
+    int done = 0;                                     // copies handed over (this thread's part)
+    auto hand_over = [&](int issued) {                // copy `done`, of `issued` so far
+      switch (issued - done) {
+        case 1: cp_wait<0>(); break;
+        case 2: cp_wait<1>(); break;
+        case 3: cp_wait<2>(); break;
+        default: cp_wait<3>(); break;
+      }
+      fence_async_smem();
+      if (done == 0) mbar_arrive(&bar->q);            // (the queries' group came first)
+      mbar_arrive(&bar->full[done % S]);
+      ++done;
+    };
+    bool ok = true;
+    for (int i = 0; i < n; ++i) {
+      const int slot = i % S, j = i / 2;
+      if (ok && i >= S) {
+        // while the slot is still read, hand over what has arrived
+        const uint32_t parity = (i / S - 1) & 1;
+        while (done < i && !mbar_test(&bar->empty[slot], parity)) hand_over(i);
+        ok = wait_one(&bar->empty[slot], parity, abort, status);
+      }
+      if (!(i & 1)) {
+        rows[(j & 1) * kT + t] = next_row;
+        ok = !loaders_sync_or(!ok);
+        if (!ok) break;
+      }
+      if (ok && in) {
+        const __nv_bfloat16* pool = (const __nv_bfloat16*)(i & 1 ? q.a.vp : q.a.kp) + c * 8;
+        const uint32_t dst = s0 + C::oRing + slot * C::kTile;
 #pragma unroll 4
-          for (int r = t / CH; r < kT; r += kT / CH) {
-            const int64_t row = rows[(j & 1) * kT + r];
-            const bool live = row >= 0 && has;
-            cp16(dst + kmajor_off(r, c * 8, C::kBlk), pool + (live ? row * d : 0), live);
-          }
+        for (int r = t / CH; r < kT; r += kT / CH) {
+          const int64_t row = rows[(j & 1) * kT + r];
+          const bool live = row >= 0 && has;
+          cp16(dst + kmajor_off(r, c * 8, C::kBlk), pool + (live ? row * d : 0), live);
         }
       }
       cp_commit();
-      if (i == 1) {
-        cp_wait<2>();
-        fence_async_smem();
-        mbar_arrive(&bar->q);
-      }
-      if (i >= LAG) {
-        cp_wait<LAG>();
-        fence_async_smem();
-        mbar_arrive(&bar->full[(i - LAG) % S]);
-      }
+      if (!(i & 1) && j + 1 < tiles) next_row = lookup(j + 1);
+      if (i - done >= 3) hand_over(i + 1);
     }
+    while (ok && done < n) hand_over(n);
     cp_wait<0>();
   } else if (go && warp == 12) {
     // ---- products
@@ -259,15 +276,15 @@ __global__ void __launch_bounds__(kThreads, 1) range_tc_kernel(const __grid_cons
       tc_fence_after();
       const int end = it.k1 - it.k0 - j * kT;         // keys of this tile
       uint32_t a[32], b[32];
-      float top = -INFINITY;
+      float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
       auto most = [&](const uint32_t (&v)[32], int c0) {
         if (end >= kT) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(v[e]));
+          for (int e = 0; e < 32; ++e) m[e & 3] = fmaxf(m[e & 3], __uint_as_float(v[e]));
         } else {
 #pragma unroll
           for (int e = 0; e < 32; ++e)
-            if (c0 + e < end) top = fmaxf(top, __uint_as_float(v[e]));
+            if (c0 + e < end) m[e & 3] = fmaxf(m[e & 3], __uint_as_float(v[e]));
         }
       };
       tmem_ld32_async(ts, a);
@@ -283,6 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1) range_tc_kernel(const __grid_cons
       tmem_wait_ld(b);
       tmem_ld32_async(ts, a);
       most(b, 96);
+      const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
       const bool move = top > ref + 8.f;              // (-inf + 8 = -inf: the first tile)
       if (__any_sync(0xffffffffu, move)) {
         const float now = move ? top : ref, f = move ? exp2f(ref - now) : 1.f;
@@ -303,18 +321,19 @@ __global__ void __launch_bounds__(kThreads, 1) range_tc_kernel(const __grid_cons
       }
       // all scores of a row are -inf, or NaN: no reference (the weights follow the scores)
       const float r = ref == -INFINITY ? 0.f : ref;
-      float sum0 = 0.f, sum1 = 0.f;
+      const F2 minus_r(-r, -r);
+      F2 sum[2] = {F2(0.f, 0.f), F2(0.f, 0.f)};
       auto weigh = [&](const uint32_t (&v)[32], int c0) {
         uint32_t w[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          float p0 = ex2(__uint_as_float(v[2 * e]) - r), p1 = ex2(__uint_as_float(v[2 * e + 1]) - r);
+          const float2 x = add2(F2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), minus_r).get();
+          float p0 = ex2(x.x), p1 = ex2(x.y);
           if (end < kT) {
             p0 = c0 + 2 * e < end ? p0 : 0.f;
             p1 = c0 + 2 * e + 1 < end ? p1 : 0.f;
           }
-          sum0 += p0;
-          sum1 += p1;
+          sum[e & 1] = add2(sum[e & 1], F2(p0, p1));
           w[e] = pack_bf16(p0, p1);
         }
         tmem_st16_async(ts + c0 / 2, w);              // over scores that were read
@@ -330,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1) range_tc_kernel(const __grid_cons
       weigh(a, 64);
       tmem_wait_ld(b);
       weigh(b, 96);
-      l += sum0 + sum1;
+      l += sum[0].sum() + sum[1].sum();
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(&bar->p[x]);
@@ -378,8 +397,7 @@ cudaError_t launch(const Params& q) {
   if (e != cudaSuccess) return e;
   const int rb = C::RT * kT;
   const dim3 grid((unsigned)(q.p.p_splits * ((q.p.all + rb - 1) / rb)), q.a.Hk);
-  range_tc_kernel<DP><<<grid, kThreads, C::kSmem, q.a.stream>>>(q);
-  return cudaGetLastError();
+  return launch_dependent(range_tc_kernel<DP>, grid, dim3(kThreads), C::kSmem, q.a.stream, q);
 }
 
 }  // namespace

@@ -26,36 +26,6 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32;   // of the backward pass
 constexpr int kRowWarps = 4;                            // of the forward pass
 
-// Two fp32 values in one 64-bit register; an operation is one instruction for both (each
-// rounded as the scalar one is).
-struct F2 {
-  uint64_t v;
-  __device__ __forceinline__ F2() {}
-  __device__ __forceinline__ F2(float x, float y) {
-    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
-  }
-  __device__ __forceinline__ explicit F2(float x) : F2(x, x) {}
-  __device__ __forceinline__ float2 get() const {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-  }
-  __device__ __forceinline__ float sum() const {
-    const float2 r = get();
-    return r.x + r.y;
-  }
-};
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-
 // A run of N elements of T as raw words, loaded and stored at once (2 to 16 bytes).
 template <typename T, int N>
 struct Run {
