@@ -447,6 +447,7 @@ cudaError_t launch_cache_attention(const CacheAttnArgs& a) {
   q.a = a;
   q.p = cache::make_plan(a);
   q.G = a.H / a.Hk;
+  q.box_rows = 0;
   q.stall = test_stall_cycles();
   return a.dtype == DARK_BF16 ? cache::launch_all<__nv_bfloat16>(q) : cache::launch_all<float>(q);
 }

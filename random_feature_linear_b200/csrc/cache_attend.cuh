@@ -36,6 +36,7 @@ struct Params {
   CacheAttnArgs a;
   Plan p;
   int G;
+  int box_rows;                           // rows of a tensor copy of the pools (0: none)
   long long stall;                        // testing stall of the tcgen05 kernel (0: none)
 };
 

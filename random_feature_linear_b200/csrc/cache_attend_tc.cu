@@ -2,16 +2,20 @@
 // whole batch share the prefix's keys, so that a range is a pair of matrix products,
 // S = Y K^T and O = P V, over tiles of 128 rows and 128 keys.
 //
-// A CTA takes one key range and up to RT tiles of 128 rows of one key head. Warps 0-3 (and
-// 4-7 for the second tile) turn scores into weights, a thread a row; warps 8-11 bring keys
-// and values; one lane of warp 12 issues the products. S and O live in TMEM; P replaces S
-// there as bf16 and is the first operand of the second product. While one tile's scores
-// are exponentiated the other tile's products run. A row's reference exponent moves only
-// when a score passes it by 2^8, so that O is rescaled a few times a range.
+// A CTA takes one key range and up to RT tiles of 128 rows of one key head. Warps 0-7 (and
+// 8-15 for the second tile) turn scores into weights, two threads a row (64 keys each; one
+// thread a row took 2100 cycles a tile, twice the products' time); warps 16-18 bring keys and
+// values; one lane of warp 19 issues the products. S and O live in TMEM; P replaces S there
+// as bf16 and is the first operand of the second product. While one tile's scores are
+// exponentiated the other tile's products run. A row's reference exponent moves only when a
+// score passes it by 2^8, so that O is rescaled a few times a range.
 //
 // Queries and weights are rounded to bf16 (the products' operand type); scores, sums and
-// exponents are fp32. Keys and values come by 16-byte asynchronous copies rather than tensor
-// copies: pages may have any size and a range may end inside one.
+// exponents are fp32. Whole tiles of keys and values come by tensor copies of as many rows as
+// divide both the page and the tile (8 at least); tiles that end inside the range's last page, and pages
+// of other sizes, by 16-byte asynchronous copies with zeros behind the end (stale rows of a
+// page may hold anything, and a weight of 0 does not cancel an infinity). Those take about
+// 2000 cycles to issue a 128 x 128 tile, twice the products' time.
 //
 // Bound by the two products (4 rows keys d operations) and the exponentials (rows keys)
 // alike: one 128 x 128 tile at d = 128 takes 1024 cycles of either unit.
@@ -28,7 +32,8 @@ namespace {
 using namespace tc;
 
 constexpr int kT = 128;                               // rows and keys of a tile
-constexpr int kThreads = 13 * 32;
+constexpr int kSoftWarps = 16, kLoad = 96;            // weights; loading threads
+constexpr int kThreads = 32 * kSoftWarps + kLoad + 32;
 
 template <int DP>
 struct Tc {
@@ -37,7 +42,8 @@ struct Tc {
   static constexpr uint32_t kTile = DP / 64 * kBlk;   // 128 rows of DP columns, bf16
   static constexpr int kSlots = (int)(131072 / kTile);  // ring of key and value tiles
   static constexpr uint32_t oQ = 0, oRing = RT * kTile, oRows = oRing + kSlots * kTile;
-  static constexpr uint32_t oBar = oRows + 2 * kT * 8, kSmem = oBar + 256 + 1024;
+  static constexpr uint32_t oMax = oRows + 2 * kT * 8;  // [tile][half][row]
+  static constexpr uint32_t oBar = oMax + RT * 2 * kT * 4, kSmem = oBar + 256 + 1024;
   static constexpr uint32_t tS = 0, tO = RT * 128, kCols = 512;
   static_assert(tO + RT * DP <= kCols, "tmem");
   static_assert(kSmem <= 232448, "shared memory");
@@ -65,16 +71,29 @@ __device__ __forceinline__ void tmem_st16_async(uint32_t taddr, const uint32_t (
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
-// Whether any of the 128 loading threads passes `bad`.
+// Whether any of the loading threads passes `bad`.
 __device__ __forceinline__ bool loaders_sync_or(bool bad) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+      "barrier.cta.red.or.pred q, 1, %2, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)bad)
+      : "r"((uint32_t)bad), "n"(kLoad)
+      : "memory");
+  return r != 0;
+}
+// The two warps that share 32 rows (barriers 2-9): whether any of their threads passes `x`.
+__device__ __forceinline__ bool pair_or(int id, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, 64, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)x), "r"(id)
       : "memory");
   return r != 0;
 }
@@ -100,8 +119,75 @@ struct Bars {
   int abort;
 };
 
+// 2^x for two values below 2^8 in the fused multiply-add units: x = n + f with n the nearest
+// whole number, 2^f by the polynomial of degree 3 with the least largest relative error on
+// [-1/2, 1/2] (Remez; 2^-13.7, against the 2^-9 of the rounding to bf16 that follows), n added
+// to the exponent. NaN stays out of range: its result is the largest finite number or NaN.
+__device__ __forceinline__ float2 ex2_fma(F2 v) {
+  float2 x = v.get();
+  asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(x.x));                  // -126
+  asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(x.y));
+  const F2 y(x.x, x.y), big(12582912.f, 12582912.f);                   // 1.5 2^23
+  const F2 n = add2(y, big), f = fma2(add2(n, F2(-12582912.f)), F2(-1.f), y);
+  F2 p = fma2(F2(0.0551716691f), f, F2(0.242611122f));
+  p = fma2(p, f, F2(0.693260985f));
+  p = fma2(p, f, F2(0.999928074f));
+  const float2 pn = p.get(), nn = n.get();
+  return make_float2(__uint_as_float(__float_as_uint(pn.x) + (__float_as_uint(nn.x) << 23)),
+                     __uint_as_float(__float_as_uint(pn.y) + (__float_as_uint(nn.y) << 23)));
+}
+
+// The exponentials are shared between the special-function units (16 a cycle) and the
+// multiply-add units, one pair of kFma there: at d = 128 the products take 1024 cycles a tile
+// and the special functions alone would take as many.
+constexpr int kFma = 4;
+
+// Weights of a thread's 64 scores (columns c0 ... of its tile; TAIL: only keys below `end`
+// count) against the reference r, as bf16 into TMEM columns tp ..., and their sum.
+template <bool TAIL>
+__device__ __forceinline__ float weigh(const uint32_t (&v)[2][32], uint32_t tp, float r, int c0, int end) {
+  const F2 minus_r(-r, -r);
+  F2 sum[2] = {F2(0.f, 0.f), F2(0.f, 0.f)};
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    uint32_t w[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const F2 x = add2(F2(__uint_as_float(v[k][2 * e]), __uint_as_float(v[k][2 * e + 1])), minus_r);
+      float2 p;
+      if (e % kFma == kFma - 1) {
+        p = ex2_fma(x);
+      } else {
+        p = x.get();
+        p = make_float2(ex2(p.x), ex2(p.y));
+      }
+      if (TAIL) {
+        const int c = c0 + 32 * k + 2 * e;
+        p.x = c < end ? p.x : 0.f;
+        p.y = c + 1 < end ? p.y : 0.f;
+      }
+      sum[e & 1] = add2(sum[e & 1], F2(p.x, p.y));
+      w[e] = pack_bf16(p.x, p.y);
+    }
+    tmem_st16_async(tp + 16 * k, w);
+  }
+  return sum[0].sum() + sum[1].sum();
+}
+template <bool TAIL>
+__device__ __forceinline__ float most(const uint32_t (&v)[2][32], int c0, int end) {
+  float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (!TAIL || c0 + 32 * k + e < end) m[e & 3] = fmaxf(m[e & 3], __uint_as_float(v[k][e]));
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
 template <int DP>
-__global__ void __launch_bounds__(kThreads, 1) range_tc_kernel(const __grid_constant__ Params q) {
+__global__ void __launch_bounds__(kThreads, 1) range_tc_kernel(const __grid_constant__ Params q,
+                                                                const __grid_constant__ CUtensorMap tm_k,
+                                                                const __grid_constant__ CUtensorMap tm_v) {
   using C = Tc<DP>;
   constexpr int RT = C::RT, S = C::kSlots, CH = DP / 8;
   static_assert(S >= 2 && S <= 8, "ring");
@@ -120,16 +206,16 @@ __global__ void __launch_bounds__(kThreads, 1) range_tc_kernel(const __grid_cons
   const int d = q.a.d, ks = (d + 15) / 16;            // steps of 16 columns
 
   if (tid == 0) {
-    mbar_init(&bar->q, 128);
+    mbar_init(&bar->q, kLoad);
     mbar_init(&bar->never, 1);
     mbar_init(&bar->drain, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar->s[i], 1);
-      mbar_init(&bar->p[i], 128);
+      mbar_init(&bar->p[i], 256);
       mbar_init(&bar->o[i], 1);
     }
     for (int i = 0; i < S; ++i) {
-      mbar_init(&bar->full[i], 128);
+      mbar_init(&bar->full[i], kLoad);
       mbar_init(&bar->empty[i], 1);
     }
     bar->abort = 0;
@@ -150,72 +236,96 @@ __global__ void __launch_bounds__(kThreads, 1) range_tc_kernel(const __grid_cons
     go = !*abort;
   }
 
-  if (go && warp >= 8 && warp < 12) {
+  if (go && warp >= kSoftWarps && warp < kSoftWarps + kLoad / 32) {
     // ---- queries, then tiles K_0, V_0, K_1, V_1, ... through the ring; a copy is handed
-    // over when this thread's part of it has arrived. The threads agree on an abort before
-    // each key tile (they share the tile's row numbers).
-    const int t = tid - 256, c = t % CH;
+    // over when this thread's part of it has arrived (tensor copies count themselves). A
+    // thread that saw an abort goes on without copying: the barriers stay matched.
+    const int t = tid - 32 * kSoftWarps, c = t % CH;
     const __nv_bfloat16* y = at<__nv_bfloat16>(q.a, q.p.o_y) + ((int64_t)hk * q.p.all + it.row0) * DP;
-    for (int r = t / CH; r < rts * kT; r += kT / CH)
+    for (int r = t / CH; r < rts * kT; r += kLoad / CH)
       cp16(s0 + C::oQ + (r / kT) * C::kTile + kmajor_off(r % kT, c * 8, C::kBlk),
            y + (r < it.nrows ? (int64_t)r * DP + c * 8 : 0), r < it.nrows);
     cp_commit();
     int64_t* rows = reinterpret_cast<int64_t*>(sm + C::oRows);
     const bool in = c < 2 * ks, has = c * 8 < d;      // (a last half step is zeros)
-    const int n = 2 * tiles;
-    // row of the cache that this thread looks up for tile j; the page a tile ahead of its use
-    auto lookup = [&](int j) {
-      const int key = it.k0 + j * kT + t;
-      if (key >= it.k1) return (int64_t)-1;
-      const int64_t row = cache_row(q.a, it.pages, key, hk);
-      if (row < 0) report(status, DARK_ERR_INVALID_ARG);
-      return row;
-    };
-    int64_t next_row = lookup(0);
+    const int n = 2 * tiles, box = q.box_rows, nb = (d + 63) / 64;
     int done = 0;                                     // copies handed over (this thread's part)
-    auto hand_over = [&](int issued) {                // copy `done`, of `issued` so far
-      switch (issued - done) {
-        case 1: cp_wait<0>(); break;
-        case 2: cp_wait<1>(); break;
-        case 3: cp_wait<2>(); break;
-        default: cp_wait<3>(); break;
-      }
+    bool q_done = false, ok = true;
+    auto hand_over = [&](int pending) {               // copy `done`, `pending` groups behind it
+      if (pending == 0) cp_wait<0>();
+      else if (pending == 1) cp_wait<1>();
+      else cp_wait<2>();
       fence_async_smem();
-      if (done == 0) mbar_arrive(&bar->q);            // (the queries' group came first)
-      mbar_arrive(&bar->full[done % S]);
-      ++done;
+      if (!q_done) mbar_arrive(&bar->q);              // (the queries' group came first)
+      q_done = true;
     };
-    bool ok = true;
     for (int i = 0; i < n; ++i) {
-      const int slot = i % S, j = i / 2;
+      const int slot = i % S, j = i / 2, key0 = it.k0 + j * kT;
+      const uint32_t dst = s0 + C::oRing + slot * C::kTile;
       if (ok && i >= S) {
         // while the slot is still read, hand over what has arrived
         const uint32_t parity = (i / S - 1) & 1;
-        while (done < i && !mbar_test(&bar->empty[slot], parity)) hand_over(i);
+        while (done < i && !mbar_test(&bar->empty[slot], parity)) {
+          hand_over(i - 1 - done);
+          mbar_arrive(&bar->full[done++ % S]);
+        }
         ok = wait_one(&bar->empty[slot], parity, abort, status);
       }
+      if (box > 0 && key0 + kT <= it.k1) {            // (then all copies before it were such)
+        if (ok) {
+          for (int x = t; x < kT / box * nb; x += kLoad) {
+            const int r = x / nb * box, cb = x % nb, key = key0 + r, pg = key / q.a.page;
+            const int id = it.pages[pg];
+            const bool good = id >= 0 && id < q.a.pages;
+            if (!good) report(status, DARK_ERR_INVALID_ARG);
+            // a page outside the cache: outside the map, zeros
+            tma_load_3d(dst + cb * C::kBlk + r * 128, i & 1 ? &tm_v : &tm_k, 64 * cb, key - pg * q.a.page,
+                        good ? id * q.a.Hk + hk : q.a.pages * q.a.Hk, &bar->full[slot]);
+          }
+        }
+        if (t == 0)
+          mbar_arrive_expect_tx(&bar->full[slot], kT * 128 * nb);
+        else
+          mbar_arrive(&bar->full[slot]);
+        ++done;
+        if (i == 1) hand_over(0);
+        continue;
+      }
       if (!(i & 1)) {
-        rows[(j & 1) * kT + t] = next_row;
+        for (int k = t; k < kT; k += kLoad) {
+          const int key = key0 + k;
+          int64_t row = -1;
+          if (key < it.k1) {
+            row = cache_row(q.a, it.pages, key, hk);
+            if (row < 0) report(status, DARK_ERR_INVALID_ARG);
+          }
+          rows[(j & 1) * kT + k] = row;
+        }
         ok = !loaders_sync_or(!ok);
-        if (!ok) break;
       }
       if (ok && in) {
         const __nv_bfloat16* pool = (const __nv_bfloat16*)(i & 1 ? q.a.vp : q.a.kp) + c * 8;
-        const uint32_t dst = s0 + C::oRing + slot * C::kTile;
 #pragma unroll 4
-        for (int r = t / CH; r < kT; r += kT / CH) {
+        for (int r = t / CH; r < kT; r += kLoad / CH) {
           const int64_t row = rows[(j & 1) * kT + r];
           const bool live = row >= 0 && has;
           cp16(dst + kmajor_off(r, c * 8, C::kBlk), pool + (live ? row * d : 0), live);
         }
       }
       cp_commit();
-      if (!(i & 1) && j + 1 < tiles) next_row = lookup(j + 1);
-      if (i - done >= 3) hand_over(i + 1);
+      if (i - done >= 2) {
+        hand_over(i - done);
+        mbar_arrive(&bar->full[done++ % S]);
+      }
     }
-    while (ok && done < n) hand_over(n);
+    while (done < n) {
+      hand_over(n - 1 - done);
+      mbar_arrive(&bar->full[done++ % S]);
+    }
     cp_wait<0>();
-  } else if (go && warp == 12) {
+    if (*abort && t == 0)                             // tensor copies may be on their way
+      for (int i = n > S ? n - S : 0; i < n; ++i) mbar_wait(&bar->full[i % S], (i / S) & 1, kWaitCycles / 8);
+  } else if (go && warp == kThreads / 32 - 1) {
     // ---- products
     if (lane == 0) {
       const uint32_t id_s = idesc(kT, kT, false, false, false);
@@ -263,52 +373,44 @@ __global__ void __launch_bounds__(kThreads, 1) range_tc_kernel(const __grid_cons
       drain_mmas(&bar->drain);
     }
     __syncwarp();
-  } else if (go && warp / 4 < rts) {
-    // ---- weights: this thread's row of tile x
-    const int x = warp / 4, row = (warp & 3) * 32 + lane;
-    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+  } else if (go && warp / 8 < rts) {
+    // ---- weights: this thread's half (64 keys) of a row of tile x
+    const int x = warp / 8, half = (warp >> 2) & 1, quad = warp & 3, row = quad * 32 + lane;
+    const int pair = 2 + x * 4 + quad;
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
     const uint32_t ts = lanes + C::tS + x * kT, to = lanes + C::tO + x * DP;
+    float* mine = reinterpret_cast<float*>(sm + C::oMax) + (x * 2 + half) * kT + row;
+    const float* other = mine + (half ? -kT : kT);
     float ref = -INFINITY, l = 0.f;
     bool ok = true;
     for (int j = 0; j < tiles; ++j) {
       ok = __all_sync(0xffffffffu, wait_one(&bar->s[x], j & 1, abort, status));
-      if (!ok) break;
-      tc_fence_after();
-      const int end = it.k1 - it.k0 - j * kT;         // keys of this tile
-      uint32_t a[32], b[32];
-      float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      auto most = [&](const uint32_t (&v)[32], int c0) {
-        if (end >= kT) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) m[e & 3] = fmaxf(m[e & 3], __uint_as_float(v[e]));
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (c0 + e < end) m[e & 3] = fmaxf(m[e & 3], __uint_as_float(v[e]));
-        }
-      };
-      tmem_ld32_async(ts, a);
-      tmem_wait_ld(a);
-      tmem_ld32_async(ts + 32, b);
-      most(a, 0);
-      tmem_wait_ld(b);
-      tmem_ld32_async(ts + 64, a);
-      most(b, 32);
-      tmem_wait_ld(a);
-      tmem_ld32_async(ts + 96, b);
-      most(a, 64);
-      tmem_wait_ld(b);
-      tmem_ld32_async(ts, a);
-      most(b, 96);
-      const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
-      const bool move = top > ref + 8.f;              // (-inf + 8 = -inf: the first tile)
-      if (__any_sync(0xffffffffu, move)) {
+      const int end = it.k1 - it.k0 - j * kT, c0 = half * 64;         // keys of this tile
+      uint32_t v[2][32];
+      float top = -INFINITY;
+      if (ok) {
+        tc_fence_after();
+        tmem_ld32_async(ts + c0, v[0]);
+        tmem_ld32_async(ts + c0 + 32, v[1]);
+        tmem_wait_ld(v[0]);
+        tmem_wait_ld(v[1]);
+        top = end >= kT ? most<false>(v, c0, end) : most<true>(v, c0, end);
+        tc_fence_before();
+      }
+      // (also: both halves have read their scores, the weights may go over them)
+      if (pair_or(pair, !ok || top > ref + 8.f)) {    // (-inf + 8 = -inf: the first tile)
+        *mine = ok ? top : nanf("");
+        pair_or(pair, false);
+        const float both = *other;
+        ok = __all_sync(0xffffffffu, ok && both == both);
+        if (!ok) break;                               // (both warps)
+        top = fmaxf(top, both);
+        const bool move = top > ref + 8.f;
         const float now = move ? top : ref, f = move ? exp2f(ref - now) : 1.f;
         ref = now;
         l *= f;
-        tmem_wait_ld(a);
-        if (j > 0) {                                  // (the scores' arrival: O is complete too)
-          for (int c = 0; c < 16 * ks; c += 16) {
+        if (j > 0) {                                  // (the scores' arrival: O is complete)
+          for (int c = 16 * half; c < 16 * ks; c += 32) {
             float o[16];
             tmem_ld16(to + c, o);
             uint32_t w[16];
@@ -316,52 +418,28 @@ __global__ void __launch_bounds__(kThreads, 1) range_tc_kernel(const __grid_cons
             for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * f);
             tmem_st16_async(to + c, w);
           }
-          tmem_wait_st();
         }
       }
+      tc_fence_after();
       // all scores of a row are -inf, or NaN: no reference (the weights follow the scores)
       const float r = ref == -INFINITY ? 0.f : ref;
-      const F2 minus_r(-r, -r);
-      F2 sum[2] = {F2(0.f, 0.f), F2(0.f, 0.f)};
-      auto weigh = [&](const uint32_t (&v)[32], int c0) {
-        uint32_t w[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float2 x = add2(F2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), minus_r).get();
-          float p0 = ex2(x.x), p1 = ex2(x.y);
-          if (end < kT) {
-            p0 = c0 + 2 * e < end ? p0 : 0.f;
-            p1 = c0 + 2 * e + 1 < end ? p1 : 0.f;
-          }
-          sum[e & 1] = add2(sum[e & 1], F2(p0, p1));
-          w[e] = pack_bf16(p0, p1);
-        }
-        tmem_st16_async(ts + c0 / 2, w);              // over scores that were read
-      };
-      tmem_wait_ld(a);
-      tmem_ld32_async(ts + 32, b);
-      weigh(a, 0);
-      tmem_wait_ld(b);
-      tmem_ld32_async(ts + 64, a);
-      weigh(b, 32);
-      tmem_wait_ld(a);
-      tmem_ld32_async(ts + 96, b);
-      weigh(a, 64);
-      tmem_wait_ld(b);
-      weigh(b, 96);
-      l += sum[0].sum() + sum[1].sum();
+      l += end >= kT ? weigh<false>(v, ts + c0 / 2, r, c0, end) : weigh<true>(v, ts + c0 / 2, r, c0, end);
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(&bar->p[x]);
     }
-    if (ok) ok = __all_sync(0xffffffffu, wait_one(&bar->o[x], 0, abort, status));
+    if (ok) {
+      ok = __all_sync(0xffffffffu, wait_one(&bar->o[rts - 1], 0, abort, status));
+      *mine = l;
+      ok = !pair_or(pair, !ok);
+    }
     if (ok) {
       tc_fence_after();
-      // sums through shared memory (the tile's queries have been read): 32 rows of 32
+      // sums through shared memory (all tiles of the ring have been read): 32 rows of 32
       // columns a warp at a time, so that rows are written in runs of 128 bytes
-      float4* box = reinterpret_cast<float4*>(sm + C::oQ + x * C::kTile + (warp & 3) * 4096);
-      const int row0 = x * kT + (warp & 3) * 32;
-      for (int c = 0; c < d; c += 32) {
+      float4* box = reinterpret_cast<float4*>(sm + C::oRing + warp * 4096);
+      const int row0 = x * kT + quad * 32;
+      for (int c = 32 * half; c < d; c += 64) {
         float o[32];
         tmem_ld32(to + c, o);
         __syncwarp();
@@ -372,13 +450,13 @@ __global__ void __launch_bounds__(kThreads, 1) range_tc_kernel(const __grid_cons
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int r = 4 * i + lane / 8, e = lane & 7;
-          const float4 v = box[r * 8 + (e ^ (r & 7))];
+          const float4 w = box[r * 8 + (e ^ (r & 7))];
           if (row0 + r < it.nrows && c + 4 * e < d)
-            *reinterpret_cast<float4*>(it.acc + (int64_t)(row0 + r) * d + c + 4 * e) = v;
+            *reinterpret_cast<float4*>(it.acc + (int64_t)(row0 + r) * d + c + 4 * e) = w;
         }
       }
-      if (x * kT + row < it.nrows)
-        *reinterpret_cast<float2*>(it.ml + 2 * (x * kT + row)) = make_float2(ref, l);
+      if (half == 0 && x * kT + row < it.nrows)
+        *reinterpret_cast<float2*>(it.ml + 2 * (x * kT + row)) = make_float2(ref, l + *other);
     }
   }
   tc_fence_before();
@@ -389,21 +467,39 @@ __global__ void __launch_bounds__(kThreads, 1) range_tc_kernel(const __grid_cons
   }
 }
 
+// A map of one pool: boxes of 64 columns and `box` rows of a page of one head.
+bool pool_map(const CacheAttnArgs& a, const void* pool, int box, CUtensorMap* map) {
+  const uint64_t dims[3] = {(uint64_t)a.d, (uint64_t)a.page, (uint64_t)a.pages * a.Hk};
+  const uint64_t strides[2] = {(uint64_t)a.d * 2, (uint64_t)a.page * a.d * 2};
+  const uint32_t b[3] = {64, (uint32_t)box, 1};
+  return encode_tmap(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, pool, dims, strides, b);
+}
+
 template <int DP>
-cudaError_t launch(const Params& q) {
+cudaError_t launch(const Params& q, const CUtensorMap& tk, const CUtensorMap& tv) {
   using C = Tc<DP>;
   static int smem_set[64];
   cudaError_t e = set_smem_limit_once((const void*)range_tc_kernel<DP>, (int)C::kSmem, smem_set);
   if (e != cudaSuccess) return e;
   const int rb = C::RT * kT;
   const dim3 grid((unsigned)(q.p.p_splits * ((q.p.all + rb - 1) / rb)), q.a.Hk);
-  return launch_dependent(range_tc_kernel<DP>, grid, dim3(kThreads), C::kSmem, q.a.stream, q);
+  return launch_dependent(range_tc_kernel<DP>, grid, dim3(kThreads), C::kSmem, q.a.stream, q, tk, tv);
 }
 
 }  // namespace
 
-cudaError_t launch_prefix_tc(const Params& q) {
-  return q.p.dp == 64 ? launch<64>(q) : q.p.dp == 128 ? launch<128>(q) : launch<256>(q);
+cudaError_t launch_prefix_tc(const Params& q0) {
+  Params q = q0;
+  CUtensorMap tk = {}, tv = {};
+  // rows of a box: a power of two that divides the page, 8 at least (the swizzle's period)
+  q.box_rows = q.a.page & -q.a.page;
+  if (q.box_rows > kT) q.box_rows = kT;
+  if (q.box_rows < 8 || (int64_t)q.a.pages * q.a.Hk >= (int64_t)1 << 31 ||
+      !pool_map(q.a, q.a.kp, q.box_rows, &tk) || !pool_map(q.a, q.a.vp, q.box_rows, &tv))
+    q.box_rows = 0;
+  return q.p.dp == 64    ? launch<64>(q, tk, tv)
+         : q.p.dp == 128 ? launch<128>(q, tk, tv)
+                         : launch<256>(q, tk, tv);
 }
 
 }  // namespace cache
