@@ -347,7 +347,7 @@ int row_block(const Plan& p, int rows) {
 // its tiles and about two tiles' time to start and end, take the least time.
 void split_tiles(const CacheAttnArgs& a, Plan* p) {
   const long long tiles = (a.prefix_len + kTcKeys - 1) / kTcKeys;
-  const long long blocks = (long long)a.Hk * ((p->all + tc_rows(p->dp) - 1) / tc_rows(p->dp));
+  const long long blocks = (long long)a.Hk * ((p->all + kTcRows - 1) / kTcRows);
   long long best = -1;
   for (long long s = 1; s <= tiles && (s == 1 || blocks * s <= 4 * 148); ++s) {
     const long long per = (tiles + s - 1) / s, cost = (blocks * s + 147) / 148 * (per + 2);
@@ -366,7 +366,7 @@ Plan make_plan(const CacheAttnArgs& a) {
   p.all = a.B * p.rows;
   p.mma = a.dtype == DARK_BF16 && a.d % 8 == 0;
   p.dp = p.mma ? (a.d <= 64 ? 64 : a.d <= 128 ? 128 : 256) : a.d;
-  p.tc = p.mma && p.all >= 64 && a.prefix_len >= 256;
+  p.tc = p.mma && p.dp <= 128 && p.all >= 64 && a.prefix_len >= 256;
   // ranges: about four CTAs an SM over key heads, row blocks and ranges
   const long long want = 4LL * 148;
   const long long pb = (long long)a.Hk * ((p.all + row_block(p, p.all) - 1) / row_block(p, p.all));

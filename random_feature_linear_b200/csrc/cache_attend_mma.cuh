@@ -11,9 +11,8 @@ namespace cache {
 inline int mma_rows(int dp, int rows) { return dp <= 128 && rows > 8 ? 16 : 8; }
 cudaError_t launch_ranges_mma(const Params& q);
 
-// Rows of a tile block of the tcgen05 kernel, keys of its tiles.
-inline int tc_rows(int dp) { return dp == 256 ? 128 : 256; }
-constexpr int kTcKeys = 128;
+// Rows of a block of the tcgen05 kernel (dp <= 128), keys of its tiles.
+constexpr int kTcRows = 256, kTcKeys = 128;
 cudaError_t launch_prefix_tc(const Params& q);
 
 // The queries y = M^T M q on the tensor cores, and the cut of the own keys.

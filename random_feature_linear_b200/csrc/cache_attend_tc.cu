@@ -4,8 +4,8 @@
 //
 // A CTA takes one key range and up to RT tiles of 128 rows of one key head. Warps 0-7 (and
 // 8-15 for the second tile) turn scores into weights, two threads a row (64 keys each; one
-// thread a row took 2100 cycles a tile, twice the products' time); warps 16-18 bring keys and
-// values; one lane of warp 19 issues the products. S and O live in TMEM; P replaces S there
+// thread a row took 2100 cycles a tile, twice the products' time); warps 16 and 17 bring keys and
+// values; one lane of warp 18 issues the products. S and O live in TMEM; P replaces S there
 // as bf16 and is the first operand of the second product. While one tile's scores are
 // exponentiated the other tile's products run. A row's reference exponent moves only when a
 // score passes it by 2^8, so that O is rescaled a few times a range.
@@ -32,12 +32,12 @@ namespace {
 using namespace tc;
 
 constexpr int kT = 128;                               // rows and keys of a tile
-constexpr int kSoftWarps = 16, kLoad = 96;            // weights; loading threads
+constexpr int kSoftWarps = 16, kLoad = 64;            // weights; loading threads
 constexpr int kThreads = 32 * kSoftWarps + kLoad + 32;
 
 template <int DP>
 struct Tc {
-  static constexpr int RT = DP == 256 ? 1 : 2;        // row tiles (TMEM: RT (128 + DP) columns)
+  static constexpr int RT = 2;                        // row tiles (TMEM: RT (128 + DP) columns)
   static constexpr int kBlk = kT * 128;               // 128 rows of 64 columns
   static constexpr uint32_t kTile = DP / 64 * kBlk;   // 128 rows of DP columns, bf16
   static constexpr int kSlots = (int)(131072 / kTile);  // ring of key and value tiles
@@ -67,6 +67,37 @@ __device__ __forceinline__ void tmem_st16_async(uint32_t taddr, const uint32_t (
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
       "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
+}
+// 64 columns of this thread's TMEM lane. Loads and wait are one statement: the registers hold
+// nothing before the wait, and a copy that the compiler puts in between would take (or lose)
+// what is not there yet. (The outputs are written before the second address is read.)
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&v)[64]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31}, [%64];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, "
+      "%42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, "
+      "%60, %61, %62, %63}, [%65];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=&r"(v[0]), "=&r"(v[1]), "=&r"(v[2]), "=&r"(v[3]), "=&r"(v[4]), "=&r"(v[5]), "=&r"(v[6]),
+        "=&r"(v[7]), "=&r"(v[8]), "=&r"(v[9]), "=&r"(v[10]), "=&r"(v[11]), "=&r"(v[12]), "=&r"(v[13]),
+        "=&r"(v[14]), "=&r"(v[15]), "=&r"(v[16]), "=&r"(v[17]), "=&r"(v[18]), "=&r"(v[19]), "=&r"(v[20]),
+        "=&r"(v[21]), "=&r"(v[22]), "=&r"(v[23]), "=&r"(v[24]), "=&r"(v[25]), "=&r"(v[26]), "=&r"(v[27]),
+        "=&r"(v[28]), "=&r"(v[29]), "=&r"(v[30]), "=&r"(v[31]), "=&r"(v[32]), "=&r"(v[33]), "=&r"(v[34]),
+        "=&r"(v[35]), "=&r"(v[36]), "=&r"(v[37]), "=&r"(v[38]), "=&r"(v[39]), "=&r"(v[40]), "=&r"(v[41]),
+        "=&r"(v[42]), "=&r"(v[43]), "=&r"(v[44]), "=&r"(v[45]), "=&r"(v[46]), "=&r"(v[47]), "=&r"(v[48]),
+        "=&r"(v[49]), "=&r"(v[50]), "=&r"(v[51]), "=&r"(v[52]), "=&r"(v[53]), "=&r"(v[54]), "=&r"(v[55]),
+        "=&r"(v[56]), "=&r"(v[57]), "=&r"(v[58]), "=&r"(v[59]), "=&r"(v[60]), "=&r"(v[61]), "=&r"(v[62]),
+        "=&r"(v[63])
+      : "r"(taddr), "r"(taddr + 32)
+      : "memory");
+}
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
 }
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -145,7 +176,7 @@ constexpr int kFma = 4;
 // Weights of a thread's 64 scores (columns c0 ... of its tile; TAIL: only keys below `end`
 // count) against the reference r, as bf16 into TMEM columns tp ..., and their sum.
 template <bool TAIL>
-__device__ __forceinline__ float weigh(const uint32_t (&v)[2][32], uint32_t tp, float r, int c0, int end) {
+__device__ __forceinline__ float weigh(const uint32_t (&v)[64], uint32_t tp, float r, int c0, int end) {
   const F2 minus_r(-r, -r);
   F2 sum[2] = {F2(0.f, 0.f), F2(0.f, 0.f)};
 #pragma unroll
@@ -153,7 +184,7 @@ __device__ __forceinline__ float weigh(const uint32_t (&v)[2][32], uint32_t tp, 
     uint32_t w[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      const F2 x = add2(F2(__uint_as_float(v[k][2 * e]), __uint_as_float(v[k][2 * e + 1])), minus_r);
+      const F2 x = add2(F2(__uint_as_float(v[32 * k + 2 * e]), __uint_as_float(v[32 * k + 2 * e + 1])), minus_r);
       float2 p;
       if (e % kFma == kFma - 1) {
         p = ex2_fma(x);
@@ -174,13 +205,11 @@ __device__ __forceinline__ float weigh(const uint32_t (&v)[2][32], uint32_t tp, 
   return sum[0].sum() + sum[1].sum();
 }
 template <bool TAIL>
-__device__ __forceinline__ float most(const uint32_t (&v)[2][32], int c0, int end) {
+__device__ __forceinline__ float most(const uint32_t (&v)[64], int c0, int end) {
   float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-  for (int k = 0; k < 2; ++k)
-#pragma unroll
-    for (int e = 0; e < 32; ++e)
-      if (!TAIL || c0 + 32 * k + e < end) m[e & 3] = fmaxf(m[e & 3], __uint_as_float(v[k][e]));
+  for (int e = 0; e < 64; ++e)
+    if (!TAIL || c0 + e < end) m[e & 3] = fmaxf(m[e & 3], __uint_as_float(v[e]));
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
@@ -190,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1) range_tc_kernel(const __grid_cons
                                                                 const __grid_constant__ CUtensorMap tm_v) {
   using C = Tc<DP>;
   constexpr int RT = C::RT, S = C::kSlots, CH = DP / 8;
-  static_assert(S >= 2 && S <= 8, "ring");
+  static_assert(S >= 4 && S <= 8, "ring");
   static_assert(sizeof(Bars) <= 256, "barriers");
   const int hk = blockIdx.y;
   const Item it = item_of(q, blockIdx.x, hk, RT * kT, true, false);
@@ -326,53 +355,70 @@ __global__ void __launch_bounds__(kThreads, 1) range_tc_kernel(const __grid_cons
     if (*abort && t == 0)                             // tensor copies may be on their way
       for (int i = n > S ? n - S : 0; i < n; ++i) mbar_wait(&bar->full[i % S], (i / S) & 1, kWaitCycles / 8);
   } else if (go && warp == kThreads / 32 - 1) {
-    // ---- products
-    if (lane == 0) {
+    // ---- products: the warp stays together, one lane issues
+    {
+      const bool lead = elect_one();
       const uint32_t id_s = idesc(kT, kT, false, false, false);
       const uint32_t id_o = idesc(kT, 16 * ks, false, true, false);
+      // operands' descriptors: steps add to the address field (one lane issues all products,
+      // so that a few instructions a product count)
+      const uint64_t dq = sdesc(s0 + C::oQ, 16, 1024), dk = sdesc(s0 + C::oRing, 16, 1024);
+      const uint64_t dv = sdesc(s0 + C::oRing, C::kBlk, 1024);
       auto scores = [&](int x, int i) {               // S_x = Y_x K^T, keys in ring copy i
-        const uint32_t a = s0 + C::oQ + x * C::kTile, b = s0 + C::oRing + (i % S) * C::kTile;
-        for (int s = 0; s < ks; ++s)
-          mma(tmem + C::tS + x * kT, sdesc(a + (s / 4) * C::kBlk + (s % 4) * 32, 16, 1024),
-              sdesc(b + (s / 4) * C::kBlk + (s % 4) * 32, 16, 1024), id_s, s > 0);
+        if (!lead) return;
+        const uint64_t a = dq + (uint32_t)(x * (C::kTile >> 4)), b = dk + (uint32_t)(i % S * (C::kTile >> 4));
+#pragma unroll
+        for (int s = 0; s < DP / 16; ++s)
+          if (s < ks) {
+            const uint32_t step = (s / 4 * C::kBlk + s % 4 * 32) >> 4;
+            mma(tmem + C::tS + x * kT, a + step, b + step, id_s, s > 0);
+          }
         mma_commit(&bar->s[x]);
       };
       auto values = [&](int x, int i, bool add) {     // O_x += P_x V, values in ring copy i
-        const uint32_t b = s0 + C::oRing + (i % S) * C::kTile;
+        if (!lead) return;
+        const uint64_t b = dv + (uint32_t)(i % S * (C::kTile >> 4));
+#pragma unroll
         for (int s = 0; s < kT / 16; ++s)
-          mma_ts(tmem + C::tO + x * DP, tmem + C::tS + x * kT + 8 * s,
-                 sdesc(b + s * 2048, C::kBlk, 1024), id_o, add || s > 0);
+          mma_ts(tmem + C::tO + x * DP, tmem + C::tS + x * kT + 8 * s, b + (s * 2048 >> 4), id_o, add || s > 0);
       };
-      bool ok = wait_one(&bar->q, 0, abort, status) && wait_one(&bar->full[0], 0, abort, status);
+      auto wait = [&](uint64_t* b, uint32_t parity) {
+        return (bool)__all_sync(0xffffffffu, wait_one(b, parity, abort, status));
+      };
+      auto commit = [&](uint64_t* b) {
+        if (lead) mma_commit(b);
+        __syncwarp();
+      };
+      bool ok = wait(&bar->q, 0) && wait(&bar->full[0], 0);
       if (ok) {
         tc_fence_after();
         for (int x = 0; x < rts; ++x) scores(x, 0);
-        mma_commit(&bar->empty[0]);
+        commit(&bar->empty[0]);
       }
       for (int j = 0; j < tiles && ok; ++j) {
         const int iv = 2 * j + 1, ik = 2 * j + 2;
         const bool more = j + 1 < tiles;
-        ok = wait_one(&bar->full[iv % S], (iv / S) & 1, abort, status);
+        ok = wait(&bar->full[iv % S], (iv / S) & 1);
         for (int x = 0; x < rts && ok; ++x) {
-          ok = wait_one(&bar->p[x], j & 1, abort, status);
+          ok = wait(&bar->p[x], j & 1);
           if (!ok) break;
           tc_fence_after();
           values(x, iv, j > 0);
-          if (x == rts - 1) mma_commit(&bar->empty[iv % S]);
+          if (x == rts - 1) commit(&bar->empty[iv % S]);
           if (!more) {
-            mma_commit(&bar->o[x]);
+            commit(&bar->o[x]);
           } else {
-            if (x == 0) ok = wait_one(&bar->full[ik % S], (ik / S) & 1, abort, status);
+            if (x == 0) ok = wait(&bar->full[ik % S], (ik / S) & 1);
             if (!ok) break;
             tc_fence_after();
             scores(x, ik);
-            if (x == rts - 1) mma_commit(&bar->empty[ik % S]);
+            if (x == rts - 1) commit(&bar->empty[ik % S]);
           }
         }
       }
-      drain_mmas(&bar->drain);
+      if (lead) drain_mmas(&bar->drain);
+      __syncwarp();
     }
-    __syncwarp();
   } else if (go && warp / 8 < rts) {
     // ---- weights: this thread's half (64 keys) of a row of tile x
     const int x = warp / 8, half = (warp >> 2) & 1, quad = warp & 3, row = quad * 32 + lane;
@@ -386,17 +432,11 @@ __global__ void __launch_bounds__(kThreads, 1) range_tc_kernel(const __grid_cons
     for (int j = 0; j < tiles; ++j) {
       ok = __all_sync(0xffffffffu, wait_one(&bar->s[x], j & 1, abort, status));
       const int end = it.k1 - it.k0 - j * kT, c0 = half * 64;         // keys of this tile
-      uint32_t v[2][32];
-      float top = -INFINITY;
-      if (ok) {
-        tc_fence_after();
-        tmem_ld32_async(ts + c0, v[0]);
-        tmem_ld32_async(ts + c0 + 32, v[1]);
-        tmem_wait_ld(v[0]);
-        tmem_wait_ld(v[1]);
-        top = end >= kT ? most<false>(v, c0, end) : most<true>(v, c0, end);
-        tc_fence_before();
-      }
+      uint32_t v[64];
+      tc_fence_after();
+      tmem_ld64(ts + c0, v);                          // (of no meaning after an abort)
+      float top = end >= kT ? most<false>(v, c0, end) : most<true>(v, c0, end);
+      tc_fence_before();
       // (also: both halves have read their scores, the weights may go over them)
       if (pair_or(pair, !ok || top > ref + 8.f)) {    // (-inf + 8 = -inf: the first tile)
         *mine = ok ? top : nanf("");
@@ -497,9 +537,7 @@ cudaError_t launch_prefix_tc(const Params& q0) {
   if (q.box_rows < 8 || (int64_t)q.a.pages * q.a.Hk >= (int64_t)1 << 31 ||
       !pool_map(q.a, q.a.kp, q.box_rows, &tk) || !pool_map(q.a, q.a.vp, q.box_rows, &tv))
     q.box_rows = 0;
-  return q.p.dp == 64    ? launch<64>(q, tk, tv)
-         : q.p.dp == 128 ? launch<128>(q, tk, tv)
-                         : launch<256>(q, tk, tv);
+  return q.p.dp == 64 ? launch<64>(q, tk, tv) : launch<128>(q, tk, tv);
 }
 
 }  // namespace cache
