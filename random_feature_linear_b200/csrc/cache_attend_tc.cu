@@ -2,13 +2,13 @@
 // whole batch share the prefix's keys, so that a range is a pair of matrix products,
 // S = Y K^T and O = P V, over tiles of 128 rows and 128 keys.
 //
-// A CTA takes one key range and up to RT tiles of 128 rows of one key head. Warps 0-7 (and
-// 8-15 for the second tile) turn scores into weights, two threads a row (64 keys each; one
-// thread a row took 2100 cycles a tile, twice the products' time); warps 16 and 17 bring keys and
-// values; one lane of warp 18 issues the products. S and O live in TMEM; P replaces S there
-// as bf16 and is the first operand of the second product. While one tile's scores are
-// exponentiated the other tile's products run. A row's reference exponent moves only when a
-// score passes it by 2^8, so that O is rescaled a few times a range.
+// A CTA takes one key range and up to RT tiles of 128 rows of one key head. Warps 0-3 (and
+// 4-7 for the second tile) turn scores into weights, a thread a row, 64 keys at a time;
+// warps 8 and 9 bring keys and values; one lane of warp 10 issues the products (a second
+// issuer, one a tile, measured 151 us against 141 at 1024 rows, 32768 keys, d = 128). S and O live
+// in TMEM; P replaces S there as bf16 and is the first operand of the second product, which
+// starts on the first 64 keys while the others are weighed. While one tile's scores are
+// exponentiated the other tile's products run.
 //
 // Queries and weights are rounded to bf16 (the products' operand type); scores, sums and
 // exponents are fp32. Whole tiles of keys and values come by tensor copies of as many rows as
@@ -32,7 +32,7 @@ namespace {
 using namespace tc;
 
 constexpr int kT = 128;                               // rows and keys of a tile
-constexpr int kSoftWarps = 16, kLoad = 64;            // weights; loading threads
+constexpr int kSoftWarps = 8, kLoad = 64;             // weights; loading threads
 constexpr int kThreads = 32 * kSoftWarps + kLoad + 32;
 
 template <int DP>
@@ -42,8 +42,7 @@ struct Tc {
   static constexpr uint32_t kTile = DP / 64 * kBlk;   // 128 rows of DP columns, bf16
   static constexpr int kSlots = (int)(131072 / kTile);  // ring of key and value tiles
   static constexpr uint32_t oQ = 0, oRing = RT * kTile, oRows = oRing + kSlots * kTile;
-  static constexpr uint32_t oMax = oRows + 2 * kT * 8;  // [tile][half][row]
-  static constexpr uint32_t oBar = oMax + RT * 2 * kT * 4, kSmem = oBar + 256 + 1024;
+  static constexpr uint32_t oBar = oRows + 2 * kT * 8, kSmem = oBar + 256 + 1024;
   static constexpr uint32_t tS = 0, tO = RT * 128, kCols = 512;
   static_assert(tO + RT * DP <= kCols, "tmem");
   static_assert(kSmem <= 232448, "shared memory");
@@ -115,20 +114,6 @@ __device__ __forceinline__ bool loaders_sync_or(bool bad) {
       : "memory");
   return r != 0;
 }
-// The two warps that share 32 rows (barriers 2-9): whether any of their threads passes `x`.
-__device__ __forceinline__ bool pair_or(int id, bool x) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, %2, 64, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"((uint32_t)x), "r"(id)
-      : "memory");
-  return r != 0;
-}
-
 // Whether the phase with the given parity has completed (does not wait).
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
@@ -144,20 +129,22 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
 
 struct Bars {
   uint64_t q, never, drain;
-  uint64_t s[2], p[2], o[2];              // per row tile: scores, weights, sums are ready
+  // per row tile: scores, weights of the first and last 64 keys, the first's products, all sums
+  uint64_t s[2], p[2][2], h[2], o[2];
   uint64_t full[8], empty[8];             // ring slots
   uint32_t tmem;
   int abort;
 };
 
-// 2^x for two values below 2^8 in the fused multiply-add units: x = n + f with n the nearest
+// 2^x for two values in the fused multiply-add units: x = n + f with n the nearest
 // whole number, 2^f by the polynomial of degree 3 with the least largest relative error on
 // [-1/2, 1/2] (Remez; 2^-13.7, against the 2^-9 of the rounding to bf16 that follows), n added
 // to the exponent. NaN stays out of range: its result is the largest finite number or NaN.
 __device__ __forceinline__ float2 ex2_fma(F2 v) {
   float2 x = v.get();
-  asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(x.x));                  // -126
-  asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(x.y));
+  // to [-126, 126]: results of 2^126 and more are made anew (kGuard)
+  asm("max.NaN.f32 %0, %0, 0fC2FC0000;\n\tmin.NaN.f32 %0, %0, 0f42FC0000;" : "+f"(x.x));
+  asm("max.NaN.f32 %0, %0, 0fC2FC0000;\n\tmin.NaN.f32 %0, %0, 0f42FC0000;" : "+f"(x.y));
   const F2 y(x.x, x.y), big(12582912.f, 12582912.f);                   // 1.5 2^23
   const F2 n = add2(y, big), f = fma2(add2(n, F2(-12582912.f)), F2(-1.f), y);
   F2 p = fma2(F2(0.0551716691f), f, F2(0.242611122f));
@@ -173,8 +160,13 @@ __device__ __forceinline__ float2 ex2_fma(F2 v) {
 // and the special functions alone would take as many.
 constexpr int kFma = 4;
 
-// Weights of a thread's 64 scores (columns c0 ... of its tile; TAIL: only keys below `end`
-// count) against the reference r, as bf16 into TMEM columns tp ..., and their sum.
+// A row's reference is the largest of its first 64 scores, and moves when the weights of 64
+// later ones sum up to more than this: bf16 and fp32 keep their relative precision at any
+// size, so that only a sum far inside fp32's range matters, and no maximum is taken meanwhile.
+constexpr float kGuard = 4294967296.f;
+
+// Weights of 64 scores of a thread's row (keys c0 ... of the tile; TAIL: only keys below
+// `end` count) against the reference r, as bf16 into TMEM columns tp ..., and their sum.
 template <bool TAIL>
 __device__ __forceinline__ float weigh(const uint32_t (&v)[64], uint32_t tp, float r, int c0, int end) {
   const F2 minus_r(-r, -r);
@@ -208,8 +200,11 @@ template <bool TAIL>
 __device__ __forceinline__ float most(const uint32_t (&v)[64], int c0, int end) {
   float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-  for (int e = 0; e < 64; ++e)
-    if (!TAIL || c0 + e < end) m[e & 3] = fmaxf(m[e & 3], __uint_as_float(v[e]));
+  for (int e = 0; e < 64; e += 2) {
+    const float a = !TAIL || c0 + e < end ? __uint_as_float(v[e]) : -INFINITY;
+    const float b = !TAIL || c0 + e + 1 < end ? __uint_as_float(v[e + 1]) : -INFINITY;
+    m[e / 2 & 3] = fmaxf(m[e / 2 & 3], fmaxf(a, b));
+  }
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
@@ -240,7 +235,9 @@ __global__ void __launch_bounds__(kThreads, 1) range_tc_kernel(const __grid_cons
     mbar_init(&bar->drain, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar->s[i], 1);
-      mbar_init(&bar->p[i], 256);
+      mbar_init(&bar->p[i][0], kT);
+      mbar_init(&bar->p[i][1], kT);
+      mbar_init(&bar->h[i], 1);
       mbar_init(&bar->o[i], 1);
     }
     for (int i = 0; i < S; ++i) {
@@ -374,112 +371,118 @@ __global__ void __launch_bounds__(kThreads, 1) range_tc_kernel(const __grid_cons
             mma(tmem + C::tS + x * kT, a + step, b + step, id_s, s > 0);
           }
         mma_commit(&bar->s[x]);
+        if (x == rts - 1) mma_commit(&bar->empty[i % S]);
       };
-      auto values = [&](int x, int i, bool add) {     // O_x += P_x V, values in ring copy i
+      // O_x += P_x V over half of the keys, values in ring copy i
+      auto values = [&](int x, int i, int half, bool add) {
         if (!lead) return;
-        const uint64_t b = dv + (uint32_t)(i % S * (C::kTile >> 4));
+        const uint64_t b = dv + (uint32_t)(i % S * (C::kTile >> 4) + half * (8192 >> 4));
+        const uint32_t a = tmem + C::tS + x * kT + half * 32;
 #pragma unroll
-        for (int s = 0; s < kT / 16; ++s)
-          mma_ts(tmem + C::tO + x * DP, tmem + C::tS + x * kT + 8 * s, b + (s * 2048 >> 4), id_o, add || s > 0);
+        for (int s = 0; s < kT / 32; ++s)
+          mma_ts(tmem + C::tO + x * DP, a + 8 * s, b + (s * 2048 >> 4), id_o, add || s > 0);
+        if (half == 0) mma_commit(&bar->h[x]);
+        else if (x == rts - 1) mma_commit(&bar->empty[i % S]);
       };
       auto wait = [&](uint64_t* b, uint32_t parity) {
         return (bool)__all_sync(0xffffffffu, wait_one(b, parity, abort, status));
-      };
-      auto commit = [&](uint64_t* b) {
-        if (lead) mma_commit(b);
-        __syncwarp();
       };
       bool ok = wait(&bar->q, 0) && wait(&bar->full[0], 0);
       if (ok) {
         tc_fence_after();
         for (int x = 0; x < rts; ++x) scores(x, 0);
-        commit(&bar->empty[0]);
       }
       for (int j = 0; j < tiles && ok; ++j) {
         const int iv = 2 * j + 1, ik = 2 * j + 2;
         const bool more = j + 1 < tiles;
         ok = wait(&bar->full[iv % S], (iv / S) & 1);
         for (int x = 0; x < rts && ok; ++x) {
-          ok = wait(&bar->p[x], j & 1);
+          ok = wait(&bar->p[x][0], j & 1);
           if (!ok) break;
           tc_fence_after();
-          values(x, iv, j > 0);
-          if (x == rts - 1) commit(&bar->empty[iv % S]);
-          if (!more) {
-            commit(&bar->o[x]);
-          } else {
-            if (x == 0) ok = wait(&bar->full[ik % S], (ik / S) & 1);
-            if (!ok) break;
-            tc_fence_after();
+          values(x, iv, 0, j > 0);
+          // (the next keys' wait ahead of the weights', off the path to the scores)
+          ok = (!more || x > 0 || wait(&bar->full[ik % S], (ik / S) & 1)) && wait(&bar->p[x][1], j & 1);
+          if (!ok) break;
+          tc_fence_after();
+          values(x, iv, 1, true);
+          if (more)
             scores(x, ik);
-            if (x == rts - 1) commit(&bar->empty[ik % S]);
-          }
+          else if (lead)
+            mma_commit(&bar->o[x]);
         }
+        __syncwarp();
       }
       if (lead) drain_mmas(&bar->drain);
       __syncwarp();
     }
-  } else if (go && warp / 8 < rts) {
-    // ---- weights: this thread's half (64 keys) of a row of tile x
-    const int x = warp / 8, half = (warp >> 2) & 1, quad = warp & 3, row = quad * 32 + lane;
-    const int pair = 2 + x * 4 + quad;
+  } else if (go && warp / 4 < rts) {
+    // ---- weights: this thread's row of tile x
+    const int x = warp / 4, quad = warp & 3, row = quad * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
     const uint32_t ts = lanes + C::tS + x * kT, to = lanes + C::tO + x * DP;
-    float* mine = reinterpret_cast<float*>(sm + C::oMax) + (x * 2 + half) * kT + row;
-    const float* other = mine + (half ? -kT : kT);
     float ref = -INFINITY, l = 0.f;
     bool ok = true;
-    for (int j = 0; j < tiles; ++j) {
+    for (int j = 0; j < tiles && ok; ++j) {
       ok = __all_sync(0xffffffffu, wait_one(&bar->s[x], j & 1, abort, status));
-      const int end = it.k1 - it.k0 - j * kT, c0 = half * 64;         // keys of this tile
-      uint32_t v[64];
+      if (!ok) break;
       tc_fence_after();
-      tmem_ld64(ts + c0, v);                          // (of no meaning after an abort)
-      float top = end >= kT ? most<false>(v, c0, end) : most<true>(v, c0, end);
-      tc_fence_before();
-      // (also: both halves have read their scores, the weights may go over them)
-      if (pair_or(pair, !ok || top > ref + 8.f)) {    // (-inf + 8 = -inf: the first tile)
-        *mine = ok ? top : nanf("");
-        pair_or(pair, false);
-        const float both = *other;
-        ok = __all_sync(0xffffffffu, ok && both == both);
-        if (!ok) break;                               // (both warps)
-        top = fmaxf(top, both);
-        const bool move = top > ref + 8.f;
-        const float now = move ? top : ref, f = move ? exp2f(ref - now) : 1.f;
-        ref = now;
-        l *= f;
-        if (j > 0) {                                  // (the scores' arrival: O is complete)
-          for (int c = 16 * half; c < 16 * ks; c += 32) {
-            float o[16];
-            tmem_ld16(to + c, o);
-            uint32_t w[16];
+      const int end = it.k1 - it.k0 - j * kT;         // keys of this tile
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        const int c0 = 64 * half;
+        const uint32_t tp = ts + 32 * half;           // (over scores that were read)
+        uint32_t v[64];
+        tmem_ld64(ts + c0, v);
+        const bool tail = end < c0 + 64, first = j == 0 && half == 0;
+        float lt = 0.f;
+        auto weights = [&]() {
+          // all scores so far are -inf, or NaN: no reference (the weights follow the scores)
+          const float r = ref == -INFINITY ? 0.f : ref;
+          lt = tail ? weigh<true>(v, tp, r, c0, end) : weigh<false>(v, tp, r, c0, end);
+        };
+        if (!first) weights();
+        // their sum tells whether a score has passed the reference too far (or is not finite)
+        if (__any_sync(0xffffffffu, first || !(lt <= kGuard))) {
+          const float top = tail ? most<true>(v, c0, end) : most<false>(v, c0, end);
+          const bool move = first || !(lt <= kGuard);
+          const float now = move ? fmaxf(ref, top) : ref, f = now > ref ? exp2f(ref - now) : 1.f;
+          ref = now;
+          l *= f;
+          if (!first) {
+            // O holds the earlier tiles (complete: the scores came after them) and, at the
+            // second half, the first one's products
+            if (half == 1) {
+              ok = __all_sync(0xffffffffu, wait_one(&bar->h[x], j & 1, abort, status));
+              if (!ok) break;
+              tc_fence_after();
+            }
+            for (int c = 0; c < 16 * ks; c += 16) {
+              float o[16];
+              tmem_ld16(to + c, o);
+              uint32_t w[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * f);
-            tmem_st16_async(to + c, w);
+              for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * f);
+              tmem_st16_async(to + c, w);
+            }
           }
+          weights();
         }
+        l += lt;
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&bar->p[x][half]);
       }
-      tc_fence_after();
-      // all scores of a row are -inf, or NaN: no reference (the weights follow the scores)
-      const float r = ref == -INFINITY ? 0.f : ref;
-      l += end >= kT ? weigh<false>(v, ts + c0 / 2, r, c0, end) : weigh<true>(v, ts + c0 / 2, r, c0, end);
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(&bar->p[x]);
     }
-    if (ok) {
-      ok = __all_sync(0xffffffffu, wait_one(&bar->o[rts - 1], 0, abort, status));
-      *mine = l;
-      ok = !pair_or(pair, !ok);
-    }
+    if (ok) ok = __all_sync(0xffffffffu, wait_one(&bar->o[0], 0, abort, status) &&
+                                           (rts == 1 || wait_one(&bar->o[1], 0, abort, status)));
     if (ok) {
       tc_fence_after();
       // sums through shared memory (all tiles of the ring have been read): 32 rows of 32
       // columns a warp at a time, so that rows are written in runs of 128 bytes
       float4* box = reinterpret_cast<float4*>(sm + C::oRing + warp * 4096);
       const int row0 = x * kT + quad * 32;
-      for (int c = 32 * half; c < d; c += 64) {
+      for (int c = 0; c < d; c += 32) {
         float o[32];
         tmem_ld32(to + c, o);
         __syncwarp();
@@ -495,8 +498,8 @@ __global__ void __launch_bounds__(kThreads, 1) range_tc_kernel(const __grid_cons
             *reinterpret_cast<float4*>(it.acc + (int64_t)(row0 + r) * d + c + 4 * e) = w;
         }
       }
-      if (half == 0 && x * kT + row < it.nrows)
-        *reinterpret_cast<float2*>(it.ml + 2 * (x * kT + row)) = make_float2(ref, l + *other);
+      if (x * kT + row < it.nrows)
+        *reinterpret_cast<float2*>(it.ml + 2 * (x * kT + row)) = make_float2(ref, l);
     }
   }
   tc_fence_before();

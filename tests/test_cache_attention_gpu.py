@@ -260,6 +260,33 @@ def test_long_prefix(D, cuda_ok, d, page):
         assert err <= 3 ** 0.5 * H8
 
 
+@pytest.mark.parametrize("scale", [12.0, 40.0])
+def test_references_follow_rising_scores(D, cuda_ok, scale):
+    """Several tiles a range, and a key late in the prefix far above all before it: its weight
+    passes those against the first scores by up to 2^400."""
+    rng = np.random.default_rng(5)
+    d, page, prefix = 64, 64, 60000
+    c = Call(D, B=40, H=4, Hk=2, d=d, page=page, prefix=prefix, lens=(5,) * 40)
+    c.geom.copy_(torch.eye(d))
+    c.proj, c.wbuf = D.dark_make_projection(torch.zeros(1, 1, d, device="cuda"), c.geom, 4,
+                                            c.proj.dtype)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    c.kp.copy_(torch.randint(0, 2, c.kp.shape, generator=g, device="cuda") * 2 - 1)
+    c.vp.copy_(torch.randn(c.vp.shape, generator=g, device="cuda"))
+    want = torch.empty_like(c.out)
+    for b in range(40):
+        for h in range(4):
+            j = int(rng.integers(0, prefix))
+            p = c.shared[j // page]
+            c.q[b, h, 0] = scale * c.kp[p, h // 2, j % page]
+            want[b, h, 0] = c.vp[p, h // 2, j % page]
+    c.run()
+    assert c.status.item() == 0
+    # scores: scale * 64 / 8 at the key, scale N(0, 1) elsewhere (below scale 5.2 of 60000 keys
+    # but for 1e-2 of all queries: 33 e^-33 of the weight at scale 12)
+    torch.testing.assert_close(c.out, want, rtol=2.0 ** -7, atol=1e-4)
+
+
 @pytest.mark.parametrize("dtype,d", [(BF, 64), (BF, 256), (BF, 36), (F, 64)])
 @pytest.mark.parametrize("what", ["nan", "inf"])
 def test_hidden_values_stay_hidden(D, cuda_ok, dtype, d, what):
