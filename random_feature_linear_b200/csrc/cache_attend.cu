@@ -24,6 +24,7 @@ namespace cache {
 namespace {
 
 constexpr int kPrepRows = 8;
+constexpr long long kPrefixCtas = 4, kOwnCtas = 4;
 
 // --------------------------------------------------- queries in fp32 (SIMT) --
 
@@ -256,60 +257,63 @@ __global__ void __launch_bounds__(128) range_kernel(const __grid_constant__ Para
 
 // -------------------------------------------------------------------- the join --
 
-// One warp a row: out = sum_i 2^(m_i - m) acc_i / sum_i 2^(m_i - m) l_i over the row's
-// prefix and own ranges, in their order. Rows that see no key give zeros. Lanes take the
-// ranges' exponents and weights 32 at a time, then float4 columns of 32 / lanes_of_d ranges
-// at once, so that the ranges' sums load without waiting for one another.
-template <typename T>
+// out = sum_i 2^(m_i - m) acc_i / sum_i 2^(m_i - m) l_i over a row's prefix and own ranges.
+// W warps a row (one for many rows, four for few), each over the ranges w, w + W, ... of
+// every 32 W; lanes take the ranges' exponents and weights 32 at a time, then float4 columns
+// of 32 / per ranges at once, so that the ranges' sums load without waiting for one another.
+// The order of the sums is fixed. Rows that see no key give zeros.
+template <typename T, int W>
 __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Params q) {
+  __shared__ float4 part[W > 1 ? W : 1][2][32];
+  __shared__ float parts[W > 1 ? W : 1][2];
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t n = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (n >= (int64_t)q.a.Hk * q.p.all) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = warp % W;
+  const int64_t n = (int64_t)blockIdx.x * (4 / W) + warp / W;
+  if (n >= (int64_t)q.a.Hk * q.p.all) return;            // (W = 4: the whole CTA)
   const int hk = (int)(n / q.p.all), row = (int)(n - (int64_t)hk * q.p.all);
   const int b = row / q.p.rows, in = row - b * q.p.rows, g = in / q.a.T, t = in - g * q.a.T;
-  const int len = sched_len(q)[b], r0 = sched_off(q)[b], r1 = sched_off(q)[b + 1];
+  const int len = sched_len(q)[b], o0 = sched_off(q)[b], o1 = sched_off(q)[b + 1];
   const bool pad = (q.a.flags & DARK_CAUSAL) && len - q.a.T + t < 0;
-  const int d = q.a.d, np = q.a.prefix_len > 0 && !pad ? q.p.p_splits : 0, no = pad ? 0 : r1 - r0;
+  const int d = q.a.d, np = q.a.prefix_len > 0 && !pad ? q.p.p_splits : 0, no = pad ? 0 : o1 - o0;
   const int total = np + no;
   const int64_t pslot = (int64_t)hk * q.p.p_splits * q.p.all + row, pstep = q.p.all;
-  const int64_t oslot = ((int64_t)hk * q.p.cap + r0) * q.p.rows + in, ostep = q.p.rows;
+  const int64_t oslot = ((int64_t)hk * q.p.cap + o0) * q.p.rows + in, ostep = q.p.rows;
   const float2* pml = at<float2>(q.a, q.p.o_pml) + pslot;
   const float2* oml = at<float2>(q.a, q.p.o_oml) + oslot;
   auto ml = [&](int i) {
     return i >= total ? make_float2(-INFINITY, 0.f) : i < np ? pml[i * pstep] : oml[(i - np) * ostep];
   };
-  // columns: `per` lanes a range (8, 16 or 32), float4 c, c + 128
+  // this warp's ranges w, w + W, ...; columns: `per` lanes a range, float4 c, c + 128
   const int per = d <= 32 ? 8 : d <= 64 ? 16 : 32, sub = lane / per, subs = 32 / per;
   const int c = 4 * (lane % per);
   const float* pa = at<float>(q.a, q.p.o_pacc) + pslot * d;
   const float* oa = at<float>(q.a, q.p.o_oacc) + oslot * d;
-  float2 mine = ml(lane);
+  float2 mine = ml(lane * W + w);
   float top = mine.x;
-  for (int i = lane + 32; i < total; i += 32) top = fmaxf(top, ml(i).x);
+  for (int i = (lane + 32) * W + w; i < total; i += 32 * W) top = fmaxf(top, ml(i).x);
   top = warp_max(top);
   const float ref = top == -INFINITY ? 0.f : top;
   float l = 0.f;
   float4 o[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-  for (int i0 = 0; i0 < total; i0 += 32) {
-    if (i0 > 0) mine = ml(i0 + lane);
+  for (int i0 = 0; i0 * W + w < total; i0 += 32) {
+    if (i0 > 0) mine = ml((i0 + lane) * W + w);
     const float f = exp2f(mine.x - ref);
     l += f * mine.y;
-    const int count = min(32, total - i0);
+    const int count = min(32, (total - w + W - 1) / W - i0);
 #pragma unroll 4
     for (int i = 0; i < count; i += subs) {
-      const int k = i0 + i + sub;
-      const float w = __shfl_sync(0xffffffffu, f, i + sub);
-      if (w == 0.f || k >= total) continue;            // no visible key: acc is not read
+      const int k = (i0 + i + sub) * W + w;
+      const float x = __shfl_sync(0xffffffffu, f, i + sub);
+      if (x == 0.f || k >= total) continue;              // no visible key: acc is not read
       const float* src = k < np ? pa + k * pstep * d : oa + (k - np) * ostep * d;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         if (c + 128 * j >= d) break;
         const float4 v = *reinterpret_cast<const float4*>(src + c + 128 * j);
-        o[j].x = fmaf(w, v.x, o[j].x);
-        o[j].y = fmaf(w, v.y, o[j].y);
-        o[j].z = fmaf(w, v.z, o[j].z);
-        o[j].w = fmaf(w, v.w, o[j].w);
+        o[j].x = fmaf(x, v.x, o[j].x);
+        o[j].y = fmaf(x, v.y, o[j].y);
+        o[j].z = fmaf(x, v.z, o[j].z);
+        o[j].w = fmaf(x, v.w, o[j].w);
       }
     }
   }
@@ -319,6 +323,32 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Param
     o[0].y += __shfl_xor_sync(0xffffffffu, o[0].y, s);
     o[0].z += __shfl_xor_sync(0xffffffffu, o[0].z, s);
     o[0].w += __shfl_xor_sync(0xffffffffu, o[0].w, s);
+  }
+  if constexpr (W > 1) {                                 // the warps' sums, in order
+    part[w][0][lane] = o[0];
+    part[w][1][lane] = o[1];
+    if (lane == 0) {
+      parts[w][0] = top;
+      parts[w][1] = l;
+    }
+    __syncthreads();
+    if (w > 0) return;
+    float all = -INFINITY;
+    for (int k = 0; k < W; ++k) all = fmaxf(all, parts[k][0]);
+    l = 0.f;
+    o[0] = o[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < W; ++k) {
+      const float f = exp2f(parts[k][0] - (all == -INFINITY ? 0.f : all));
+      l = fmaf(f, parts[k][1], l);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float4 v = part[k][j][lane];
+        o[j].x = fmaf(f, v.x, o[j].x);
+        o[j].y = fmaf(f, v.y, o[j].y);
+        o[j].z = fmaf(f, v.z, o[j].z);
+        o[j].w = fmaf(f, v.w, o[j].w);
+      }
+    }
   }
   T* dst = (T*)q.a.out + b * q.a.os[0] + (int64_t)(hk * q.G + g) * q.a.os[1] + t * q.a.os[2];
   bool bad = false;
@@ -367,9 +397,11 @@ Plan make_plan(const CacheAttnArgs& a) {
   p.mma = a.dtype == DARK_BF16 && a.d % 8 == 0;
   p.dp = p.mma ? (a.d <= 64 ? 64 : a.d <= 128 ? 128 : 256) : a.d;
   p.tc = p.mma && p.dp <= 128 && p.all >= 64 && a.prefix_len >= 256;
-  // ranges: about four CTAs an SM over key heads, row blocks and ranges
-  const long long want = 4LL * 148;
-  const long long pb = (long long)a.Hk * ((p.all + row_block(p, p.all) - 1) / row_block(p, p.all));
+  p.share = p.mma && !p.tc && p.all > 16 && a.prefix_len > 0;
+  // ranges: about as many CTAs (over key heads, row blocks and ranges) as run at once
+  const long long want = kPrefixCtas * 148, want_own = kOwnCtas * 148;
+  const int prb = p.share ? kShareRows : row_block(p, p.all);
+  const long long pb = (long long)a.Hk * ((p.all + prb - 1) / prb);
   const int steps = (a.prefix_len + kKeyStep - 1) / kKeyStep;
   long long s = (want + pb - 1) / pb;
   if (s > (steps + 1) / 2) s = (steps + 1) / 2;
@@ -378,7 +410,7 @@ Plan make_plan(const CacheAttnArgs& a) {
   p.p_splits = steps == 0 ? 1 : (a.prefix_len + p.p_chunk - 1) / p.p_chunk;
   if (p.tc) split_tiles(a, &p);
   const long long ob = (long long)a.Hk * ((p.rows + row_block(p, p.rows) - 1) / row_block(p, p.rows));
-  p.cap = a.B + (int)((want + ob - 1) / ob);
+  p.cap = a.B + (int)((want_own + ob - 1) / ob);
   size_t o = kWsHeader;
   auto take = [&](size_t n) {
     const size_t at = o;
@@ -424,6 +456,7 @@ cudaError_t launch_all(const Params& q) {
   if (e != cudaSuccess) return e;
   if (q.p.mma) {
     if (q.p.tc) e = launch_prefix_tc(q);
+    if (q.p.share) e = launch_prefix_mma(q);
     if (e == cudaSuccess) e = launch_ranges_mma(q);
     if (e != cudaSuccess) return e;
   } else {
@@ -434,7 +467,10 @@ cudaError_t launch_all(const Params& q) {
     }
   }
   const int64_t rows = (int64_t)q.a.Hk * q.p.all;
-  return launch_dependent(join_kernel<T>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, q.a.stream, q);
+  // a warp a row while that gives every SM about eight warps
+  return rows >= 8 * num_sms()
+             ? launch_dependent(join_kernel<T, 1>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, q.a.stream, q)
+             : launch_dependent(join_kernel<T, 4>, dim3((unsigned)rows), dim3(128), 0, q.a.stream, q);
 }
 
 }  // namespace

@@ -1,9 +1,12 @@
 // Cache attention, key ranges on the tensor cores for few rows (bf16).
 //
-// A CTA of four warps takes one key range and a block of 8 or 16 rows. Every warp
-// streams its own tiles of 16 keys (tiles w, w + 4, ...) through a private ring in
-// shared memory (cp.async, 16 bytes a lane, no barrier between warps) and keeps its own
-// reference exponents, weights and sums; the four are joined once at the end.
+// A CTA takes one key range and a block of rows, in one of two ways:
+//  * few rows (a sequence's own keys; a prefix with up to 16 rows): every warp streams its
+//    own tiles of 16 keys (tiles w, w + warps, ...) through a private ring in shared memory
+//    (cp.async, 16 bytes a lane, no barrier between warps) for the same 8 or 16 rows, and
+//    keeps its own reference exponents, weights and sums, joined once at the end;
+//  * a prefix with more rows: all warps share each tile of keys, brought by all of them, and
+//    take 8 rows each, so that the keys are read once for 8 rows a warp.
 //
 // mma.sync m16n8k16 has 16 rows; eight queries fill it twice, as y = hi + lo: rows 0-7
 // hold hi, rows 8-15 lo, and a thread's accumulators of rows g and g + 8 add up to the
@@ -22,7 +25,7 @@ namespace dark {
 namespace cache {
 namespace {
 
-constexpr int kWarps = 4, kKeys = 16;
+constexpr int kKeys = 16;
 
 __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
   uint32_t v;
@@ -44,38 +47,42 @@ __device__ __forceinline__ bool tile_non_finite(uint32_t tile, int lane) {
   return __any_sync(0xffffffffu, bad);
 }
 
-template <int DP>
+// Shared memory of a CTA: rings of `kStages` tiles for each of W warps, or one for all.
+// Two to four CTAs an SM, so that one's first copies run under another's products.
+template <int DP, bool SHARE>
 struct Cfg {
   static constexpr uint32_t kTile = kKeys * DP * 2;       // one matrix of a tile
-  static constexpr int kStages = DP == 64 ? 6 : 3;
-  static constexpr uint32_t kWarpBytes = kStages * 2 * kTile;
-  static constexpr uint32_t kSmem = kWarps * kWarpBytes;
+  static constexpr int W = SHARE || DP <= 128 ? 4 : 2;
+  static constexpr int kStages = SHARE ? 6 : DP == 64 ? 4 : 3;
+  static constexpr uint32_t kRing = kStages * 2 * kTile;
+  static constexpr uint32_t kSmem = SHARE ? kRing : W * kRing;
 };
 
-// RT: row tiles of eight rows.
-template <int DP, int RT>
-__global__ void __launch_bounds__(kWarps * 32) range_mma_kernel(const __grid_constant__ Params q) {
-  using C = Cfg<DP>;
+// RT: row tiles of eight rows a warp. SHARE: the warps take different rows.
+template <int DP, int RT, bool SHARE>
+__global__ void __launch_bounds__(Cfg<DP, SHARE>::W * 32) range_mma_kernel(const __grid_constant__ Params q) {
+  using C = Cfg<DP, SHARE>;
   constexpr int NS = DP / 16, NT = DP / 8;                // k-steps of a score, column tiles
-  constexpr int RB = 8 * RT, S = C::kStages;
+  constexpr int W = C::W, RB = 8 * RT * (SHARE ? W : 1), S = C::kStages;
   const int hk = blockIdx.y;
   pdl_wait();
   pdl_launch();
-  const Item it = item_of(q, blockIdx.x, hk, RB, q.a.prefix_len > 0 && !q.p.tc, true);
+  const Item it = item_of(q, blockIdx.x, hk, RB, SHARE || (q.a.prefix_len > 0 && !q.p.tc && !q.p.share), !SHARE);
   if (!it.any) return;
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  uint8_t* ring = smem + warp * C::kWarpBytes;
-  const uint32_t ring0 = tc::smem_u32(ring);
+  const int r0 = SHARE ? warp * 8 * RT : 0;               // this warp's first row of the block
+  const uint32_t ring0 = tc::smem_u32(smem) + (SHARE ? 0 : warp * C::kRing);
   const int d = q.a.d, chunks = d / 8;
   const __nv_bfloat16* kp = (const __nv_bfloat16*)q.a.kp;
   const __nv_bfloat16* vp = (const __nv_bfloat16*)q.a.vp;
 
-  // rows of the cache that this warp's tile i holds, one key a lane (lanes 0-15)
+  // rows of the cache that the (warp's) tile i holds, one key a lane (lanes 0-15)
   const int ntiles = (it.k1 - it.k0 + kKeys - 1) / kKeys;
-  const int mine = ntiles > warp ? (ntiles - warp + kWarps - 1) / kWarps : 0;
+  const int mine = SHARE ? ntiles : ntiles > warp ? (ntiles - warp + W - 1) / W : 0;
+  auto first_key = [&](int i) { return it.k0 + (SHARE ? i : warp + i * W) * kKeys; };
   auto lookup = [&](int i) -> int64_t {
-    const int key = it.k0 + (warp + i * kWarps) * kKeys + (lane & 15);
+    const int key = first_key(i) + (lane & 15);
     if (i >= mine || key >= it.k1) return -1;
     const int64_t row = cache_row(q.a, it.pages, key, hk);
     if (row < 0) report(q.a.dev_status, DARK_ERR_INVALID_ARG);
@@ -83,10 +90,11 @@ __global__ void __launch_bounds__(kWarps * 32) range_mma_kernel(const __grid_con
   };
   auto issue = [&](int i, int64_t row) {                  // zeros past the range and past d
     const uint32_t k0 = ring0 + (uint32_t)(i % S) * 2 * C::kTile, v0 = k0 + C::kTile;
-    constexpr int CH = DP / 8;
+    constexpr int CH = DP / 8, T = SHARE ? W * 32 : 32;
+    const int me = SHARE ? tid : lane;
 #pragma unroll
-    for (int n = 0; n < kKeys * CH / 32; ++n) {
-      const int idx = n * 32 + lane, r = idx / CH, c = idx % CH;
+    for (int n = 0; n < kKeys * CH / T; ++n) {
+      const int idx = n * T + me, r = idx / CH, c = idx % CH;
       const int64_t at = __shfl_sync(0xffffffffu, row, r);
       const bool ok = at >= 0 && c < chunks;
       const int64_t o = ok ? at * d + c * 8 : 0;
@@ -111,7 +119,7 @@ __global__ void __launch_bounds__(kWarps * 32) range_mma_kernel(const __grid_con
     const int64_t lo = (int64_t)q.a.Hk * q.p.all * DP;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      const int row = rt * 8 + g;
+      const int row = r0 + rt * 8 + g;
       const bool ok = row < it.nrows;
       const __nv_bfloat16* src = y + ((int64_t)hk * q.p.all + it.row0 + (ok ? row : 0)) * DP + 2 * t;
 #pragma unroll
@@ -141,7 +149,7 @@ __global__ void __launch_bounds__(kWarps * 32) range_mma_kernel(const __grid_con
   const int lr = lane & 7, lg = lane >> 3;                // ldmatrix: row in, and number of, a matrix
   for (int i = 0; i < mine; ++i) {
     cp_wait<S - 2>();
-    __syncwarp();
+    if (SHARE) __syncthreads(); else __syncwarp();        // (the slot of tile i - 1 is free too)
     {
       const int64_t row = next;
       next = lookup(i + S);
@@ -166,7 +174,7 @@ __global__ void __launch_bounds__(kWarps * 32) range_mma_kernel(const __grid_con
         mma16816_bf16(s[rt][1], ya[rt][st], b[2], b[3]);
       }
     }
-    const int key0 = it.k0 + (warp + i * kWarps) * kKeys + 2 * t;
+    const int key0 = first_key(i) + 2 * t;
     uint32_t pa[RT][4];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
@@ -207,7 +215,7 @@ __global__ void __launch_bounds__(kWarps * 32) range_mma_kernel(const __grid_con
     }
     // A weight of 0 does not cancel an infinite or NaN value of a key that only other rows
     // see (causal, the last T - 1 keys): a tile with one adds its values key by key.
-    const int tile0 = it.k0 + (warp + i * kWarps) * kKeys;
+    const int tile0 = first_key(i);
     if (tile0 + kKeys > seen_by_all && tile_non_finite<DP>(v0, lane)) {
 #pragma unroll 1
       for (int kk = 0; kk < kKeys; ++kk) {
@@ -226,7 +234,7 @@ __global__ void __launch_bounds__(kWarps * 32) range_mma_kernel(const __grid_con
           }
         }
       }
-      __syncwarp();
+      if (!SHARE) __syncwarp();
       continue;
     }
 #pragma unroll
@@ -239,19 +247,33 @@ __global__ void __launch_bounds__(kWarps * 32) range_mma_kernel(const __grid_con
         mma16816_bf16(o[rt][n + 1], pa[rt], b[2], b[3]);
       }
     }
-    __syncwarp();                                         // the slot may be filled again
+    if (!SHARE) __syncwarp();                             // the slot may be filled again
   }
   cp_wait<0>();
 
-  // join the four warps: references and weights, then sums (in the rings' memory)
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
     l[rt] += __shfl_xor_sync(0xffffffffu, l[rt], 1);
     l[rt] += __shfl_xor_sync(0xffffffffu, l[rt], 2);
   }
+  if constexpr (SHARE) {                                  // a warp's rows are its own
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      const int row = r0 + rt * 8 + g;
+      if (row >= it.nrows) continue;
+      float* dst = it.acc + (int64_t)row * d + 2 * t;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        if (8 * n < d)
+          *reinterpret_cast<float2*>(dst + 8 * n) = make_float2(o[rt][n][0] + o[rt][n][2], o[rt][n][1] + o[rt][n][3]);
+      if (t == 0) *reinterpret_cast<float2*>(it.ml + 2 * row) = make_float2(ref[rt], l[rt]);
+    }
+    return;
+  }
+  // join the warps: references and weights, then sums (in the rings' memory)
   __syncthreads();
   float* sml = reinterpret_cast<float*>(smem);            // [warp][RB][2]
-  float* sac = sml + kWarps * RB * 2;                     // [warp][RB][DP]
+  float* sac = sml + W * RB * 2;                          // [warp][RB][DP]
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
     const int row = rt * 8 + g;
@@ -266,16 +288,16 @@ __global__ void __launch_bounds__(kWarps * 32) range_mma_kernel(const __grid_con
           make_float2(o[rt][n][0] + o[rt][n][2], o[rt][n][1] + o[rt][n][3]);
   }
   __syncthreads();
-  for (int idx = tid; idx < it.nrows * (d / 4); idx += kWarps * 32) {
+  for (int idx = tid; idx < it.nrows * (d / 4); idx += W * 32) {
     const int row = idx / (d / 4), c = (idx - row * (d / 4)) * 4;
     float top = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sml[(w * RB + row) * 2]);
+    for (int w = 0; w < W; ++w) top = fmaxf(top, sml[(w * RB + row) * 2]);
     const float r = top == -INFINITY ? 0.f : top;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     float lw = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < W; ++w) {
       const float f = exp2f(sml[(w * RB + row) * 2] - r);
       const float4 x = *reinterpret_cast<const float4*>(sac + (w * RB + row) * DP + c);
       lw = fmaf(f, sml[(w * RB + row) * 2 + 1], lw);
@@ -290,25 +312,32 @@ __global__ void __launch_bounds__(kWarps * 32) range_mma_kernel(const __grid_con
   }
 }
 
-template <int DP, int RT>
+template <int DP, int RT, bool SHARE>
 cudaError_t launch(const Params& q, long long n) {
-  using C = Cfg<DP>;
+  using C = Cfg<DP, SHARE>;
   static int smem_set[64];
-  cudaError_t e = set_smem_limit_once((const void*)range_mma_kernel<DP, RT>, (int)C::kSmem, smem_set);
+  cudaError_t e = set_smem_limit_once((const void*)range_mma_kernel<DP, RT, SHARE>, (int)C::kSmem, smem_set);
   if (e != cudaSuccess) return e;
-  return launch_dependent(range_mma_kernel<DP, RT>, dim3((unsigned)n, q.a.Hk), dim3(kWarps * 32),
+  return launch_dependent(range_mma_kernel<DP, RT, SHARE>, dim3((unsigned)n, q.a.Hk), dim3(C::W * 32),
                           C::kSmem, q.a.stream, q);
 }
 
 }  // namespace
 
+cudaError_t launch_prefix_mma(const Params& q) {
+  const long long n = (long long)q.p.p_splits * ((q.p.all + kShareRows - 1) / kShareRows);
+  return q.p.dp == 64    ? launch<64, 1, true>(q, n)
+         : q.p.dp == 128 ? launch<128, 1, true>(q, n)
+                         : launch<256, 1, true>(q, n);
+}
+
 cudaError_t launch_ranges_mma(const Params& q) {
   const int dp = q.p.dp, rb = mma_rows(dp, q.p.rows);
   long long n = (long long)q.p.cap * ((q.p.rows + rb - 1) / rb);
-  if (q.a.prefix_len > 0 && !q.p.tc) n += (long long)q.p.p_splits * ((q.p.all + rb - 1) / rb);
-  if (dp == 256) return launch<256, 1>(q, n);
-  if (dp == 128) return rb == 8 ? launch<128, 1>(q, n) : launch<128, 2>(q, n);
-  return rb == 8 ? launch<64, 1>(q, n) : launch<64, 2>(q, n);
+  if (q.a.prefix_len > 0 && !q.p.tc && !q.p.share) n += (long long)q.p.p_splits * ((q.p.all + rb - 1) / rb);
+  if (dp == 256) return launch<256, 1, false>(q, n);
+  if (dp == 128) return rb == 8 ? launch<128, 1, false>(q, n) : launch<128, 2, false>(q, n);
+  return rb == 8 ? launch<64, 1, false>(q, n) : launch<64, 2, false>(q, n);
 }
 
 }  // namespace cache

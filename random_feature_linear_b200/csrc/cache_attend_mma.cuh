@@ -11,6 +11,10 @@ namespace cache {
 inline int mma_rows(int dp, int rows) { return dp <= 128 && rows > 8 ? 16 : 8; }
 cudaError_t launch_ranges_mma(const Params& q);
 
+// The prefix's ranges for more rows, which share the keys in a CTA.
+constexpr int kShareRows = 32;
+cudaError_t launch_prefix_mma(const Params& q);
+
 // Rows of a block of the tcgen05 kernel (dp <= 128), keys of its tiles.
 constexpr int kTcRows = 256, kTcKeys = 128;
 cudaError_t launch_prefix_tc(const Params& q);
