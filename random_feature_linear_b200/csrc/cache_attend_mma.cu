@@ -56,6 +56,7 @@ struct Cfg {
   static constexpr int kStages = SHARE ? 6 : DP == 64 ? 4 : 3;
   static constexpr uint32_t kRing = kStages * 2 * kTile;
   static constexpr uint32_t kSmem = SHARE ? kRing : W * kRing;
+  static_assert(SHARE || kSmem >= W * 16 * (DP + 8 + 2) * 4, "the join's sums");
 };
 
 // RT: row tiles of eight rows a warp. SHARE: the warps take different rows.
@@ -77,38 +78,70 @@ __global__ void __launch_bounds__(Cfg<DP, SHARE>::W * 32) range_mma_kernel(const
   const __nv_bfloat16* kp = (const __nv_bfloat16*)q.a.kp;
   const __nv_bfloat16* vp = (const __nv_bfloat16*)q.a.vp;
 
-  // rows of the cache that the (warp's) tile i holds, one key a lane (lanes 0-15)
+  // Where tile i's keys lie: the page (its number is loaded a tile ahead of its use) and row
+  // in it of one key a lane (lanes 0-15), or, where no tile reaches over a page's end and rows
+  // are not padded, of the tile's first key: then the tile is one run of memory.
+  const bool flat = q.a.page % kKeys == 0 && d == DP;
   const int ntiles = (it.k1 - it.k0 + kKeys - 1) / kKeys;
   const int mine = SHARE ? ntiles : ntiles > warp ? (ntiles - warp + W - 1) / W : 0;
   auto first_key = [&](int i) { return it.k0 + (SHARE ? i : warp + i * W) * kKeys; };
-  auto lookup = [&](int i) -> int64_t {
-    const int key = first_key(i) + (lane & 15);
-    if (i >= mine || key >= it.k1) return -1;
-    const int64_t row = cache_row(q.a, it.pages, key, hk);
-    if (row < 0) report(q.a.dev_status, DARK_ERR_INVALID_ARG);
-    return row;
+  struct Spot {
+    int id, in;                                           // in < 0: no key
   };
-  auto issue = [&](int i, int64_t row) {                  // zeros past the range and past d
+  auto lookup = [&](int i) {
+    const int key = first_key(i) + (flat ? 0 : lane & 15);
+    Spot s{0, -1};
+    if (i < mine && key < it.k1) {
+      const int pg = key / q.a.page;
+      s.in = key - pg * q.a.page;
+      s.id = it.pages[pg];
+    }
+    return s;
+  };
+  auto issue = [&](int i, Spot s) {                       // zeros past the range and past d
     const uint32_t k0 = ring0 + (uint32_t)(i % S) * 2 * C::kTile, v0 = k0 + C::kTile;
     constexpr int CH = DP / 8, T = SHARE ? W * 32 : 32;
     const int me = SHARE ? tid : lane;
+    int64_t row = -1;
+    if (s.in >= 0) {
+      if (s.id >= 0 && s.id < q.a.pages)
+        row = ((int64_t)s.id * q.a.Hk + hk) * q.a.page + s.in;
+      else
+        report(q.a.dev_status, DARK_ERR_INVALID_ARG);
+    }
+    if (flat) {
+      const int live = row < 0 ? 0 : (it.k1 - first_key(i)) * CH;      // 16-byte pieces
+      const int64_t o = row < 0 ? 0 : row * DP + me * 8;
 #pragma unroll
-    for (int n = 0; n < kKeys * CH / T; ++n) {
-      const int idx = n * T + me, r = idx / CH, c = idx % CH;
-      const int64_t at = __shfl_sync(0xffffffffu, row, r);
-      const bool ok = at >= 0 && c < chunks;
-      const int64_t o = ok ? at * d + c * 8 : 0;
-      cp16(k0 + tile_off<DP>(r, c), kp + o, ok);
-      cp16(v0 + tile_off<DP>(r, c), vp + o, ok);
+      for (int n = 0; n < kKeys * CH / T; ++n) {
+        const int idx = n * T + me;
+        const bool ok = idx < live;
+        const uint32_t to = tile_off<DP>(idx / CH, idx % CH);
+        cp16(k0 + to, kp + (ok ? o + n * T * 8 : 0), ok);
+        cp16(v0 + to, vp + (ok ? o + n * T * 8 : 0), ok);
+      }
+    } else {
+#pragma unroll
+      for (int n = 0; n < kKeys * CH / T; ++n) {
+        const int idx = n * T + me, r = idx / CH, c = idx % CH;
+        const int64_t at = __shfl_sync(0xffffffffu, row, r);
+        const bool ok = at >= 0 && c < chunks;
+        const int64_t o = ok ? at * d + c * 8 : 0;
+        cp16(k0 + tile_off<DP>(r, c), kp + o, ok);
+        cp16(v0 + tile_off<DP>(r, c), vp + o, ok);
+      }
     }
   };
-  int64_t next = lookup(0);
+  Spot next = lookup(S - 1);
+  {
+    Spot s[S - 1];
 #pragma unroll
-  for (int i = 0; i < S - 1; ++i) {
-    const int64_t row = next;
-    next = lookup(i + 1);
-    if (i < mine) issue(i, row);
-    cp_commit();
+    for (int i = 0; i < S - 1; ++i) s[i] = lookup(i);
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) {
+      if (i < mine) issue(i, s[i]);
+      cp_commit();
+    }
   }
 
   // the rows' queries as A fragments: hi in rows 0-7, lo in rows 8-15
@@ -151,9 +184,9 @@ __global__ void __launch_bounds__(Cfg<DP, SHARE>::W * 32) range_mma_kernel(const
     cp_wait<S - 2>();
     if (SHARE) __syncthreads(); else __syncwarp();        // (the slot of tile i - 1 is free too)
     {
-      const int64_t row = next;
+      const Spot s = next;
       next = lookup(i + S);
-      if (i + S - 1 < mine) issue(i + S - 1, row);
+      if (i + S - 1 < mine) issue(i + S - 1, s);
       cp_commit();
     }
     const uint32_t k0 = ring0 + (uint32_t)(i % S) * 2 * C::kTile, v0 = k0 + C::kTile;
@@ -273,7 +306,9 @@ __global__ void __launch_bounds__(Cfg<DP, SHARE>::W * 32) range_mma_kernel(const
   // join the warps: references and weights, then sums (in the rings' memory)
   __syncthreads();
   float* sml = reinterpret_cast<float*>(smem);            // [warp][RB][2]
-  float* sac = sml + W * RB * 2;                          // [warp][RB][DP]
+  // rows 8 words apart from a multiple of the 32 banks: a warp's 8 rows share none
+  constexpr int LD = DP + 8;
+  float* sac = sml + W * RB * 2;                          // [warp][RB][LD]
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
     const int row = rt * 8 + g;
@@ -281,7 +316,7 @@ __global__ void __launch_bounds__(Cfg<DP, SHARE>::W * 32) range_mma_kernel(const
       sml[(warp * RB + row) * 2] = ref[rt];
       sml[(warp * RB + row) * 2 + 1] = l[rt];
     }
-    float* dst = sac + (warp * RB + row) * DP + 2 * t;
+    float* dst = sac + (warp * RB + row) * LD + 2 * t;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
       *reinterpret_cast<float2*>(dst + 8 * n) =
@@ -299,7 +334,7 @@ __global__ void __launch_bounds__(Cfg<DP, SHARE>::W * 32) range_mma_kernel(const
 #pragma unroll
     for (int w = 0; w < W; ++w) {
       const float f = exp2f(sml[(w * RB + row) * 2] - r);
-      const float4 x = *reinterpret_cast<const float4*>(sac + (w * RB + row) * DP + c);
+      const float4 x = *reinterpret_cast<const float4*>(sac + (w * RB + row) * LD + c);
       lw = fmaf(f, sml[(w * RB + row) * 2 + 1], lw);
       a.x = fmaf(f, x.x, a.x); a.y = fmaf(f, x.y, a.y);
       a.z = fmaf(f, x.z, a.z); a.w = fmaf(f, x.w, a.w);

@@ -113,13 +113,14 @@ __global__ void __launch_bounds__(WARPS * 32) queries_mma_kernel(const __grid_co
   }
   cp_wait<0>();
   __syncthreads();
-  // the warps' sums, in order of the warps
-  float* sum = reinterpret_cast<float*>(smem);         // [warp][16][DP]
+  // the warps' sums, in order of the warps; rows 8 words apart from a multiple of the 32 banks
+  constexpr int LD = DP + 8;
+  float* sum = reinterpret_cast<float*>(smem);         // [warp][16][LD]
 #pragma unroll
   for (int k = 0; k < NT; ++k) {
-    float* to = sum + (warp * 16 + g) * DP + 8 * k + 2 * t;
+    float* to = sum + (warp * 16 + g) * LD + 8 * k + 2 * t;
     *reinterpret_cast<float2*>(to) = make_float2(o[k][0], o[k][1]);
-    *reinterpret_cast<float2*>(to + 8 * DP) = make_float2(o[k][2], o[k][3]);
+    *reinterpret_cast<float2*>(to + 8 * LD) = make_float2(o[k][2], o[k][3]);
   }
   __syncthreads();
   const int gg = h % q.G, hk = h / q.G;
@@ -129,7 +130,7 @@ __global__ void __launch_bounds__(WARPS * 32) queries_mma_kernel(const __grid_co
     if (k >= n) break;
     float v = 0.f;
 #pragma unroll
-    for (int x = 0; x < WARPS; ++x) v += sum[(x * 16 + row) * DP + c];
+    for (int x = 0; x < WARPS; ++x) v += sum[(x * 16 + row) * LD + c];
     const int b = k / q.a.T, tt = k - b * q.a.T;
     store_query_hi_lo(at<__nv_bfloat16>(q.a, q.p.o_y), rows,
                       (int64_t)hk * q.p.all + (b * q.G + gg) * q.a.T + tt, DP, c, v);
@@ -139,7 +140,7 @@ __global__ void __launch_bounds__(WARPS * 32) queries_mma_kernel(const __grid_co
 template <int DP, int WARPS>
 cudaError_t launch(const Params& q) {
   static int smem_set[64];
-  const int smem = (int)max((1 + 2 * WARPS) * Cfg<DP>::kTile, (uint32_t)WARPS * 16 * DP * 4);
+  const int smem = (int)max((1 + 2 * WARPS) * Cfg<DP>::kTile, (uint32_t)WARPS * 16 * (DP + 8) * 4);
   cudaError_t e = set_smem_limit_once((const void*)queries_mma_kernel<DP, WARPS>, smem, smem_set);
   if (e != cudaSuccess) return e;
   const int n = q.a.B * q.a.T;
