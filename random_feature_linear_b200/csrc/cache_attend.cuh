@@ -90,7 +90,7 @@ __device__ __forceinline__ Item item_of(const Params& q, int x, int hk, int rb, 
   if (!own) return it;
   const int nb = (p.rows + rb - 1) / rb;
   const int r = x / nb, blk = x % nb;
-  const int4 v = sched_range(q)[r];
+  const int4 v = __ldcg(sched_range(q) + r);
   it.pages = q.a.table + (int64_t)v.x * q.a.max_pages;
   it.k0 = v.y;
   it.k1 = v.z;

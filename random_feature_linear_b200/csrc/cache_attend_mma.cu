@@ -66,10 +66,17 @@ __global__ void __launch_bounds__(Cfg<DP, SHARE>::W * 32) range_mma_kernel(const
   constexpr int NS = DP / 16, NT = DP / 8;                // k-steps of a score, column tiles
   constexpr int W = C::W, RB = 8 * RT * (SHARE ? W : 1), S = C::kStages;
   const int hk = blockIdx.y;
-  pdl_wait();
+  // After a launch for the prefix the own ranges need nothing of it and start while it runs:
+  // it began after the queries' launch had ended, so what that wrote is in L2 (read past L1).
+  // The wait at the end then makes this launch's end that of both, for the join.
+  const bool late = !SHARE && (q.p.tc || q.p.share);
+  if (!late) pdl_wait();
   pdl_launch();
   const Item it = item_of(q, blockIdx.x, hk, RB, SHARE || (q.a.prefix_len > 0 && !q.p.tc && !q.p.share), !SHARE);
-  if (!it.any) return;
+  if (!it.any) {
+    if (late) pdl_wait();
+    return;
+  }
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int r0 = SHARE ? warp * 8 * RT : 0;               // this warp's first row of the block
@@ -94,7 +101,7 @@ __global__ void __launch_bounds__(Cfg<DP, SHARE>::W * 32) range_mma_kernel(const
     if (i < mine && key < it.k1) {
       const int pg = key / q.a.page;
       s.in = key - pg * q.a.page;
-      s.id = it.pages[pg];
+      s.id = __ldcg(it.pages + pg);
     }
     return s;
   };
@@ -157,10 +164,10 @@ __global__ void __launch_bounds__(Cfg<DP, SHARE>::W * 32) range_mma_kernel(const
       const __nv_bfloat16* src = y + ((int64_t)hk * q.p.all + it.row0 + (ok ? row : 0)) * DP + 2 * t;
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
-        ya[rt][s][0] = ok ? *reinterpret_cast<const uint32_t*>(src + 16 * s) : 0u;
-        ya[rt][s][1] = ok ? *reinterpret_cast<const uint32_t*>(src + lo + 16 * s) : 0u;
-        ya[rt][s][2] = ok ? *reinterpret_cast<const uint32_t*>(src + 16 * s + 8) : 0u;
-        ya[rt][s][3] = ok ? *reinterpret_cast<const uint32_t*>(src + lo + 16 * s + 8) : 0u;
+        ya[rt][s][0] = ok ? __ldcg(reinterpret_cast<const uint32_t*>(src + 16 * s)) : 0u;
+        ya[rt][s][1] = ok ? __ldcg(reinterpret_cast<const uint32_t*>(src + lo + 16 * s)) : 0u;
+        ya[rt][s][2] = ok ? __ldcg(reinterpret_cast<const uint32_t*>(src + 16 * s + 8)) : 0u;
+        ya[rt][s][3] = ok ? __ldcg(reinterpret_cast<const uint32_t*>(src + lo + 16 * s + 8)) : 0u;
       }
       lim[rt] = ok ? visible_keys(q, it, row) : 0;
       if (ok) seen_by_all = min(seen_by_all, lim[rt]);
@@ -345,6 +352,7 @@ __global__ void __launch_bounds__(Cfg<DP, SHARE>::W * 32) range_mma_kernel(const
       it.ml[2 * row + 1] = lw;
     }
   }
+  if (late) pdl_wait();
 }
 
 template <int DP, int RT, bool SHARE>

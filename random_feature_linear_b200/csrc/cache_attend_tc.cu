@@ -40,7 +40,7 @@ struct Tc {
   static constexpr int RT = 2;                        // row tiles (TMEM: RT (128 + DP) columns)
   static constexpr int kBlk = kT * 128;               // 128 rows of 64 columns
   static constexpr uint32_t kTile = DP / 64 * kBlk;   // 128 rows of DP columns, bf16
-  static constexpr int kSlots = (int)(131072 / kTile);  // ring of key and value tiles
+  static constexpr int kSlots = 4;                    // ring of key and value tiles
   static constexpr uint32_t oQ = 0, oRing = RT * kTile, oRows = oRing + kSlots * kTile;
   static constexpr uint32_t oBar = oRows + 2 * kT * 8, kSmem = oBar + 256 + 1024;
   static constexpr uint32_t tS = 0, tO = RT * 128, kCols = 512;
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1) range_tc_kernel(const __grid_cons
                                                                 const __grid_constant__ CUtensorMap tm_v) {
   using C = Tc<DP>;
   constexpr int RT = C::RT, S = C::kSlots, CH = DP / 8;
-  static_assert(S >= 4 && S <= 8, "ring");
+  static_assert(S >= 4 && S <= 8 && S % 2 == 0, "ring");
   static_assert(sizeof(Bars) <= 256, "barriers");
   const int hk = blockIdx.y;
   const Item it = item_of(q, blockIdx.x, hk, RT * kT, true, false);
@@ -267,14 +267,18 @@ __global__ void __launch_bounds__(kThreads, 1) range_tc_kernel(const __grid_cons
     // over when this thread's part of it has arrived (tensor copies count themselves). A
     // thread that saw an abort goes on without copying: the barriers stay matched.
     const int t = tid - 32 * kSoftWarps, c = t % CH;
-    const __nv_bfloat16* y = at<__nv_bfloat16>(q.a, q.p.o_y) + ((int64_t)hk * q.p.all + it.row0) * DP;
-    for (int r = t / CH; r < rts * kT; r += kLoad / CH)
-      cp16(s0 + C::oQ + (r / kT) * C::kTile + kmajor_off(r % kT, c * 8, C::kBlk),
-           y + (r < it.nrows ? (int64_t)r * DP + c * 8 : 0), r < it.nrows);
-    cp_commit();
-    int64_t* rows = reinterpret_cast<int64_t*>(sm + C::oRows);
     const bool in = c < 2 * ks, has = c * 8 < d;      // (a last half step is zeros)
     const int n = 2 * tiles, box = q.box_rows, nb = (d + 63) / 64;
+    auto tensor_tile = [&](int key0) { return box > 0 && key0 + kT <= it.k1; };
+    auto load_queries = [&]() {
+      const __nv_bfloat16* y = at<__nv_bfloat16>(q.a, q.p.o_y) + ((int64_t)hk * q.p.all + it.row0) * DP;
+      for (int r = t / CH; r < rts * kT; r += kLoad / CH)
+        cp16(s0 + C::oQ + (r / kT) * C::kTile + kmajor_off(r % kT, c * 8, C::kBlk),
+             y + (r < it.nrows ? (int64_t)r * DP + c * 8 : 0), r < it.nrows);
+      cp_commit();
+    };
+    if (!tensor_tile(it.k0)) load_queries();          // (else after the first tensor copies)
+    int64_t* rows = reinterpret_cast<int64_t*>(sm + C::oRows);
     int done = 0;                                     // copies handed over (this thread's part)
     bool q_done = false, ok = true;
     auto hand_over = [&](int pending) {               // copy `done`, `pending` groups behind it
@@ -297,11 +301,11 @@ __global__ void __launch_bounds__(kThreads, 1) range_tc_kernel(const __grid_cons
         }
         ok = wait_one(&bar->empty[slot], parity, abort, status);
       }
-      if (box > 0 && key0 + kT <= it.k1) {            // (then all copies before it were such)
+      if (tensor_tile(key0)) {                        // (then all copies before it were such)
         if (ok) {
           for (int x = t; x < kT / box * nb; x += kLoad) {
             const int r = x / nb * box, cb = x % nb, key = key0 + r, pg = key / q.a.page;
-            const int id = it.pages[pg];
+            const int id = __ldcg(it.pages + pg);
             const bool good = id >= 0 && id < q.a.pages;
             if (!good) report(status, DARK_ERR_INVALID_ARG);
             // a page outside the cache: outside the map, zeros
@@ -314,7 +318,10 @@ __global__ void __launch_bounds__(kThreads, 1) range_tc_kernel(const __grid_cons
         else
           mbar_arrive(&bar->full[slot]);
         ++done;
-        if (i == 1) hand_over(0);
+        if (i == 1) {
+          load_queries();
+          hand_over(0);
+        }
         continue;
       }
       if (!(i & 1)) {
