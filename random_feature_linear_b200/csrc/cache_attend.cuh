@@ -23,7 +23,7 @@ struct Plan {
   int dp;                                 // columns of the stored queries (d, padded)
   int mma;                                // bf16 with 16-byte rows: tensor cores
   int tc;                                 // the prefix by 128-row tiles (tcgen05)
-  int share;                              // the prefix by blocks of kShareRows rows
+  int share;                              // the prefix by blocks of share_rows() rows
   int p_splits, p_chunk;                  // ranges of the prefix, keys of a range
   int cap;                                // own ranges of all sequences, at most
   // byte offsets into the workspace

@@ -192,6 +192,17 @@ CASES = {
                                    q_scale=12.0, lens=tuple(range(2, 102, 5))),
     "many-rows-page-of-one": dict(B=17, H=4, Hk=1, page=1, d=128, r=64, prefix=300,
                                   lens=tuple(range(17))),
+    # a prefix that a CTA's warps share: up to 32 rows, more of them, with d 256
+    "shared-32": dict(B=3, H=10, Hk=1, d=64, page=64, prefix=500, lens=(5, 0, 90)),
+    "shared-48-d128": dict(B=6, H=8, Hk=1, d=128, r=64, page=16, prefix=200,
+                           lens=(5, 0, 90, 1, 31, 32)),
+    "shared-70-d256": dict(B=7, H=10, Hk=1, d=256, r=32, page=128, prefix=333,
+                           lens=(5, 0, 90, 1, 31, 32, 128)),
+    "shared-40-odd": dict(B=5, H=8, Hk=1, d=96, r=96, page=7, prefix=101, lens=(5, 0, 9, 1, 31)),
+    # nine to sixteen rows of a sequence, and more, over its own keys
+    "rows-12": dict(B=2, H=6, Hk=2, T=4, d=64, page=16, lens=(100, 3), causal=True),
+    "rows-40-d256": dict(B=2, H=4, Hk=1, T=10, d=256, r=64, page=16, lens=(100, 7), causal=True),
+    "rows-20-odd": dict(B=2, H=4, Hk=1, T=5, d=128, page=20, r=64, lens=(101, 3), causal=True),
     "fp32": dict(dtype=F, B=3, H=6, Hk=2, T=3, d=40, r=24, page=24, prefix=100, lens=(77, 3, 30),
                  causal=True),
     "fp32-many-rows": dict(dtype=F, B=10, H=8, Hk=2, T=2, d=64, page=16, prefix=200,
