@@ -269,15 +269,11 @@ __global__ void __launch_bounds__(kThreads, 1) range_tc_kernel(const __grid_cons
     const int t = tid - 32 * kSoftWarps, c = t % CH;
     const bool in = c < 2 * ks, has = c * 8 < d;      // (a last half step is zeros)
     const int n = 2 * tiles, box = q.box_rows, nb = (d + 63) / 64;
-    auto tensor_tile = [&](int key0) { return box > 0 && key0 + kT <= it.k1; };
-    auto load_queries = [&]() {
-      const __nv_bfloat16* y = at<__nv_bfloat16>(q.a, q.p.o_y) + ((int64_t)hk * q.p.all + it.row0) * DP;
-      for (int r = t / CH; r < rts * kT; r += kLoad / CH)
-        cp16(s0 + C::oQ + (r / kT) * C::kTile + kmajor_off(r % kT, c * 8, C::kBlk),
-             y + (r < it.nrows ? (int64_t)r * DP + c * 8 : 0), r < it.nrows);
-      cp_commit();
-    };
-    if (!tensor_tile(it.k0)) load_queries();          // (else after the first tensor copies)
+    const __nv_bfloat16* y = at<__nv_bfloat16>(q.a, q.p.o_y) + ((int64_t)hk * q.p.all + it.row0) * DP;
+    for (int r = t / CH; r < rts * kT; r += kLoad / CH)
+      cp16(s0 + C::oQ + (r / kT) * C::kTile + kmajor_off(r % kT, c * 8, C::kBlk),
+           y + (r < it.nrows ? (int64_t)r * DP + c * 8 : 0), r < it.nrows);
+    cp_commit();
     int64_t* rows = reinterpret_cast<int64_t*>(sm + C::oRows);
     int done = 0;                                     // copies handed over (this thread's part)
     bool q_done = false, ok = true;
@@ -301,11 +297,11 @@ __global__ void __launch_bounds__(kThreads, 1) range_tc_kernel(const __grid_cons
         }
         ok = wait_one(&bar->empty[slot], parity, abort, status);
       }
-      if (tensor_tile(key0)) {                        // (then all copies before it were such)
+      if (box > 0 && key0 + kT <= it.k1) {            // (then all copies before it were such)
         if (ok) {
           for (int x = t; x < kT / box * nb; x += kLoad) {
             const int r = x / nb * box, cb = x % nb, key = key0 + r, pg = key / q.a.page;
-            const int id = __ldcg(it.pages + pg);
+            const int id = it.pages[pg];
             const bool good = id >= 0 && id < q.a.pages;
             if (!good) report(status, DARK_ERR_INVALID_ARG);
             // a page outside the cache: outside the map, zeros
@@ -318,10 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1) range_tc_kernel(const __grid_cons
         else
           mbar_arrive(&bar->full[slot]);
         ++done;
-        if (i == 1) {
-          load_queries();
-          hand_over(0);
-        }
+        if (i == 1) hand_over(0);
         continue;
       }
       if (!(i & 1)) {
