@@ -23,93 +23,143 @@ namespace dark {
 namespace cache {
 namespace {
 
-constexpr int kPrepRows = 8;
+constexpr int kPrepRows = 8, kPrepTile = 32;         // (256 threads: one a row of M and query)
 constexpr long long kPrefixCtas = 4, kOwnCtas = 4;
 
 // --------------------------------------------------- queries in fp32 (SIMT) --
 
-// y of kPrepRows rows of one query head: p = (c_m M) q, y = 2 (c_m M)^T p. Threads over
-// the rows of M, then over the columns; sums in fp32.
+// y of kPrepRows rows of one query head: p = 2 (c_m M) q, y = (c_m M)^T p, kPrepTile rows of
+// c_m M at a time through shared memory (read once for both products): a thread a (row of
+// M, query) for p, then a thread a column of all queries for y. Sums in fp32.
 template <typename T>
 __global__ void __launch_bounds__(256) queries_kernel(const __grid_constant__ Params q) {
   using W = typename WeightOf<T>::type;
+  pdl_launch();
   if (blockIdx.x == gridDim.x - 1) {
     if (blockIdx.y == 0) make_sched(q);
     return;
   }
   extern __shared__ float sm[];
-  const int d = q.a.d, r = q.a.r, tid = threadIdx.x;
-  float* x = sm;                          // [d][kPrepRows]
-  float* p = sm + kPrepRows * d;          // [r][kPrepRows]
+  const int d = q.a.d, r = q.a.r, tid = threadIdx.x, ld = d + 1;
+  float* x = sm;                                         // [kPrepRows][ld]
+  float* wt = x + kPrepRows * ld;                        // [kPrepTile][ld]
+  float* p = wt + kPrepTile * ld;                        // [kPrepTile][kPrepRows]
   const int h = blockIdx.y, n0 = blockIdx.x * kPrepRows;     // rows (b, t) of head h
   const int n = q.a.B * q.a.T;
   const W* w = (const W*)q.a.w + ((int64_t)(q.a.heads_w == 1 ? 0 : h) * (q.a.m + r) + q.a.m) * d;
-  for (int i = tid; i < kPrepRows * d; i += blockDim.x) {
+  for (int i = tid; i < kPrepRows * d; i += 256) {
     const int row = i / d, c = i - row * d, k = n0 + row;
     float v = 0.f;
     if (k < n) {
       const int b = k / q.a.T, t = k - b * q.a.T;
       v = to_f32(((const T*)q.a.q)[b * q.a.qs[0] + h * q.a.qs[1] + t * q.a.qs[2] + c]);
     }
-    x[c * kPrepRows + row] = v;
+    x[row * ld + c] = v;
   }
-  __syncthreads();
-  for (int i = tid; i < r; i += blockDim.x) {
-    float s[kPrepRows];
+  float s[kPrepRows];
 #pragma unroll
-    for (int k = 0; k < kPrepRows; ++k) s[k] = 0.f;
-    for (int c = 0; c < d; ++c) {
-      const float u = to_f32(w[(int64_t)i * d + c]);
-#pragma unroll
-      for (int k = 0; k < kPrepRows; ++k) s[k] = fmaf(u, x[c * kPrepRows + k], s[k]);
+  for (int k = 0; k < kPrepRows; ++k) s[k] = 0.f;
+  for (int i0 = 0; i0 < r; i0 += kPrepTile) {
+    const int here = min(kPrepTile, r - i0);
+    __syncthreads();                                     // the last tile's readers are done
+#pragma unroll 8
+    for (int i = tid; i < here * d; i += 256) {
+      const int row = i / d;
+      wt[row * ld + i - row * d] = to_f32(w[(int64_t)i0 * d + i]);
     }
+    __syncthreads();
+    {
+      const int i = tid / kPrepRows, k = tid % kPrepRows;
+      float v[4] = {0.f, 0.f, 0.f, 0.f};
+      if (i < here)
+        for (int c = 0; c < d; c += 4)
 #pragma unroll
-    for (int k = 0; k < kPrepRows; ++k) p[i * kPrepRows + k] = 2.f * s[k];
-  }
-  __syncthreads();
-  const int g = h % q.G, hk = h / q.G, dp = q.p.dp;
-  for (int c = tid; c < dp; c += blockDim.x) {
-    float s[kPrepRows];
-#pragma unroll
-    for (int k = 0; k < kPrepRows; ++k) s[k] = 0.f;
-    if (c < d)
-      for (int i = 0; i < r; ++i) {
-        const float u = to_f32(w[(int64_t)i * d + c]);
+          for (int e = 0; e < 4; ++e) v[e] = fmaf(wt[i * ld + c + e], x[k * ld + c + e], v[e]);
+      p[i * kPrepRows + k] = 2.f * ((v[0] + v[1]) + (v[2] + v[3]));
+    }
+    __syncthreads();
+    if (tid < d)
+      for (int i = 0; i < here; ++i) {
+        const float u = wt[i * ld + tid];
 #pragma unroll
         for (int k = 0; k < kPrepRows; ++k) s[k] = fmaf(u, p[i * kPrepRows + k], s[k]);
       }
+  }
+  const int g = h % q.G, hk = h / q.G;
+  if (tid < d)
     for (int k = 0; k < kPrepRows && n0 + k < n; ++k) {
       const int b = (n0 + k) / q.a.T, t = (n0 + k) - b * q.a.T;
-      const int64_t row = (int64_t)hk * q.p.all + (b * q.G + g) * q.a.T + t;
-      at<float>(q.a, q.p.o_y)[row * dp + c] = s[k];
+      at<float>(q.a, q.p.o_y)[((int64_t)hk * q.p.all + (b * q.G + g) * q.a.T + t) * q.p.dp + tid] = s[k];
     }
-  }
 }
 
 // ------------------------------------------------------ ranges in fp32 (SIMT) --
 
-// RB rows against one key range, KT keys at a time: 128 threads as RB / 4 row groups of
-// four rows. Scores and sums are register tiles of four rows (by 1-2 keys, by up to 16
-// columns); the running exponent and weight of a row live in shared memory. Bound by
-// fp32 multiply-adds for many rows, by the key and value rows for few.
-template <typename T, int RB, int KT>
-__global__ void __launch_bounds__(128) range_kernel(const __grid_constant__ Params q, int prefix) {
-  constexpr int RG = RB / 4, CG = 128 / RG, KJ = KT / CG, NJ = (256 + 4 * CG - 1) / (4 * CG);
-  static_assert(KT % CG == 0, "keys over column groups");
+// RB rows against one key range, KT keys at a time: NT threads as RB / 4 row groups of four
+// rows. Scores and sums are register tiles of four rows (by KT / CG keys, by up to 16
+// columns); the running exponent and weight of a row live in shared memory. Keys and values
+// have a buffer each, so that the next keys load under the softmax and the values' product,
+// the next values under the next scores; a tile's page numbers are looked up a tile ahead.
+// Bound by fp32 multiply-adds for many rows, by the key and value rows' latency for few.
+template <typename T, int RB, int KT, int NT>
+__global__ void __launch_bounds__(NT) range_kernel(const __grid_constant__ Params q, int prefix, int own) {
+  constexpr int RG = RB / 4, CG = NT / RG, KJ = KT / CG, NJ = (256 + 4 * CG - 1) / (4 * CG);
+  static_assert(KT % CG == 0 && KT <= NT, "keys over column groups");
   const int hk = blockIdx.y;
-  const Item it = item_of(q, blockIdx.x, hk, RB, prefix != 0, prefix == 0);
+  pdl_wait();
+  pdl_launch();
+  const Item it = item_of(q, blockIdx.x, hk, RB, prefix != 0, own != 0);
   if (!it.any) return;
   extern __shared__ __align__(16) float sm[];
   const int d = q.a.d, ld = d + 4, tid = threadIdx.x;
   float* ys = sm;                         // [RB][ld]
-  float* kv = ys + RB * ld;               // [KT][ld]: keys, then values
-  float* sc = kv + KT * ld;               // [KT][RB + 4]: scores, then weights
+  float* ks = ys + RB * ld;               // [KT][ld]
+  float* vs = ks + KT * ld;               // [KT][ld]
+  float* sc = vs + KT * ld;               // [KT][RB + 4]: scores, then weights
   float* mx = sc + KT * (RB + 4);         // [RB] reference exponent
   float* lw = mx + RB;                    // [RB] weight
   float* fac = lw + RB;                   // [RB] factor of the sums so far
   int* lim = (int*)(fac + RB);            // [RB] visible keys
+  int64_t* rows = (int64_t*)(lim + RB);   // [2][KT] rows of the cache
   const float* y = at<float>(q.a, q.p.o_y) + ((int64_t)hk * q.p.all + it.row0) * q.p.dp;
-  for (int i = tid; i < RB * d; i += 128) {
+
+  auto lookup = [&](int j0) {                            // one key a thread
+    if (tid >= KT || j0 + tid >= it.k1) return (int64_t)-1;
+    const int64_t row = cache_row(q.a, it.pages, j0 + tid, hk);
+    if (row < 0) report(q.a.dev_status, DARK_ERR_INVALID_ARG);
+    return row;
+  };
+  auto fill = [&](const void* pool, float* dst, int tile) {            // zeros past the range
+    const int per = d / 4;
+    int k = tid / per, c = tid - k * per;
+    const int dk = NT / per, dc = NT - dk * per;
+    for (; k < KT;) {
+      const int64_t row = rows[(tile & 1) * KT + k];
+      const T* src = (const T*)pool + (row < 0 ? 0 : row * d + 4 * c);
+      float* to = dst + k * ld + 4 * c;
+      if constexpr (sizeof(T) == 4) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         (uint32_t)__cvta_generic_to_shared(to)),
+                     "l"(src), "r"(row < 0 ? 0 : 16)
+                     : "memory");
+      } else {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (row >= 0) v = make_float4(to_f32(src[0]), to_f32(src[1]), to_f32(src[2]), to_f32(src[3]));
+        *reinterpret_cast<float4*>(to) = v;
+      }
+      k += dk;
+      c += dc;
+      if (c >= per) {
+        c -= per;
+        ++k;
+      }
+    }
+    cp_commit();
+  };
+
+  int64_t next = lookup(it.k0);
+  if (tid < KT) rows[tid] = next;
+  for (int i = tid; i < RB * d; i += NT) {
     const int row = i / d, c = i - row * d;
     ys[row * ld + c] = row < it.nrows ? y[(int64_t)row * q.p.dp + c] : 0.f;
   }
@@ -126,44 +176,27 @@ __global__ void __launch_bounds__(128) range_kernel(const __grid_constant__ Para
     for (int j = 0; j < NJ; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[r][j][e] = 0.f;
+  __syncthreads();
+  fill(q.a.kp, ks, 0);
+  fill(q.a.vp, vs, 0);
 
-  auto fill = [&](const void* pool, int j0) {          // KT rows; zeros past the range
-    const int per = d / 4;
-    for (int i = tid; i < KT * per; i += 128) {
-      const int k = i / per, c = (i - k * per) * 4;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (j0 + k < it.k1) {
-        const int64_t row = cache_row(q.a, it.pages, j0 + k, hk);
-        if (row >= 0) {
-          const T* src = (const T*)pool + row * d + c;
-          if constexpr (sizeof(T) == 4) {
-            v = *reinterpret_cast<const float4*>(src);
-          } else {
-            v = make_float4(to_f32(src[0]), to_f32(src[1]), to_f32(src[2]), to_f32(src[3]));
-          }
-        } else {
-          report(q.a.dev_status, DARK_ERR_INVALID_ARG);
-        }
-      }
-      *reinterpret_cast<float4*>(kv + k * ld + c) = v;
-    }
-  };
-
-  for (int j0 = it.k0; j0 < it.k1; j0 += KT) {
-    __syncthreads();                                   // the last tile's readers are done
-    fill(q.a.kp, j0);
+  for (int j0 = it.k0, tile = 0; j0 < it.k1; j0 += KT, ++tile) {
+    const bool more = j0 + KT < it.k1;
+    next = lookup(j0 + KT);
+    cp_wait<1>();                                        // the keys
     __syncthreads();
     float s[4][KJ];
 #pragma unroll
     for (int r = 0; r < 4; ++r)
 #pragma unroll
       for (int k = 0; k < KJ; ++k) s[r][k] = 0.f;
+#pragma unroll 2
     for (int c = 0; c < d; c += 4) {
       float4 a[4], b[KJ];
 #pragma unroll
       for (int r = 0; r < 4; ++r) a[r] = *reinterpret_cast<const float4*>(ys + (rg * 4 + r) * ld + c);
 #pragma unroll
-      for (int k = 0; k < KJ; ++k) b[k] = *reinterpret_cast<const float4*>(kv + (cg + k * CG) * ld + c);
+      for (int k = 0; k < KJ; ++k) b[k] = *reinterpret_cast<const float4*>(ks + (cg + k * CG) * ld + c);
 #pragma unroll
       for (int r = 0; r < 4; ++r)
 #pragma unroll
@@ -181,10 +214,11 @@ __global__ void __launch_bounds__(128) range_kernel(const __grid_constant__ Para
         const int key = j0 + cg + k * CG, row = rg * 4 + r;
         sc[(cg + k * CG) * (RB + 4) + row] = key < it.k1 && key < lim[row] ? s[r][k] : -INFINITY;
       }
+    if (more && tid < KT) rows[((tile + 1) & 1) * KT + tid] = next;
     __syncthreads();
-    fill(q.a.vp, j0);
-    // a warp takes rows warp, warp + 4, ...: exponent, weights, factor
-    for (int row = tid >> 5; row < RB; row += 4) {
+    if (more) fill(q.a.kp, ks, tile + 1); else cp_commit();
+    // a warp takes rows warp, warp + warps, ...: exponent, weights, factor
+    for (int row = tid >> 5; row < RB; row += NT / 32) {
       float top = -INFINITY;
       for (int k = tid & 31; k < KT; k += 32) top = fmaxf(top, sc[k * (RB + 4) + row]);
       top = warp_max(top);
@@ -203,6 +237,7 @@ __global__ void __launch_bounds__(128) range_kernel(const __grid_constant__ Para
         mx[row] = now;
       }
     }
+    cp_wait<1>();                                        // the values
     __syncthreads();
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -216,18 +251,18 @@ __global__ void __launch_bounds__(128) range_kernel(const __grid_constant__ Para
     int all = nk;                                      // keys that all four rows see
 #pragma unroll
     for (int r = 0; r < 4; ++r) all = min(all, lim[rg * 4 + r] - j0);
-    for (int k = 0; k < nk; ++k) {
+    auto add = [&](int k, bool masked) {
       const float4 p = *reinterpret_cast<const float4*>(sc + k * (RB + 4) + rg * 4);
       const float pr[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
         const int c = (cg + j * CG) * 4;
         if (c < d) {
-          const float4 v = *reinterpret_cast<const float4*>(kv + k * ld + c);
+          const float4 v = *reinterpret_cast<const float4*>(vs + k * ld + c);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             // a weight of 0 does not cancel an infinite or NaN value behind the mask
-            if (k >= all && j0 + k >= lim[rg * 4 + r]) continue;
+            if (masked && j0 + k >= lim[rg * 4 + r]) continue;
             acc[r][j][0] = fmaf(pr[r], v.x, acc[r][j][0]);
             acc[r][j][1] = fmaf(pr[r], v.y, acc[r][j][1]);
             acc[r][j][2] = fmaf(pr[r], v.z, acc[r][j][2]);
@@ -235,6 +270,14 @@ __global__ void __launch_bounds__(128) range_kernel(const __grid_constant__ Para
           }
         }
       }
+    };
+    int k = 0;
+#pragma unroll 4
+    for (; k < all; ++k) add(k, false);
+    for (; k < nk; ++k) add(k, true);
+    if (more) {
+      __syncthreads();
+      fill(q.a.vp, vs, tile + 1);
     }
   }
 #pragma unroll
@@ -370,7 +413,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Param
 
 int row_block(const Plan& p, int rows) {
   if (p.mma) return mma_rows(p.rows);
-  return rows >= 32 ? 32 : 8;
+  return rows >= 32 ? 64 : 8;
 }
 
 // Ranges of the tcgen05 kernel (one CTA an SM): the count whose waves of CTAs, each with
@@ -428,18 +471,26 @@ Plan make_plan(const CacheAttnArgs& a) {
   return p;
 }
 
-template <typename T, int RB, int KT>
-cudaError_t launch_range(const Params& q, bool prefix) {
+template <typename T, int RB, int KT, int NT>
+cudaError_t launch_range(const Params& q, bool prefix, bool own) {
   static int smem_set[64];
-  const int d = q.a.d;
-  const size_t smem = ((size_t)(RB + KT) * (d + 4) + (size_t)KT * (RB + 4) + 4 * RB) * 4;
-  const size_t most = ((size_t)(RB + KT) * 260 + (size_t)KT * (RB + 4) + 4 * RB) * 4;
-  cudaError_t e = set_smem_limit_once((const void*)range_kernel<T, RB, KT>, (int)most, smem_set);
+  auto bytes = [](size_t d) {
+    return ((RB + 2 * KT) * (d + 4) + (size_t)KT * (RB + 4) + 4 * RB) * 4 + 2 * KT * 8;
+  };
+  auto* kernel = range_kernel<T, RB, KT, NT>;
+  cudaError_t e = set_smem_limit_once((const void*)kernel, (int)bytes(256), smem_set);
   if (e != cudaSuccess) return e;
-  const int rows = prefix ? q.p.all : q.p.rows;
-  const long long n = (long long)(prefix ? q.p.p_splits : q.p.cap) * ((rows + RB - 1) / RB);
-  range_kernel<T, RB, KT><<<dim3((unsigned)n, q.a.Hk), 128, smem, q.a.stream>>>(q, prefix ? 1 : 0);
-  return cudaGetLastError();
+  long long n = 0;
+  if (prefix) n += (long long)q.p.p_splits * ((q.p.all + RB - 1) / RB);
+  if (own) n += (long long)q.p.cap * ((q.p.rows + RB - 1) / RB);
+  return launch_dependent(kernel, dim3((unsigned)n, q.a.Hk), dim3(NT), bytes(q.a.d), q.a.stream, q,
+                          prefix ? 1 : 0, own ? 1 : 0);
+}
+// 64 rows a CTA where there are 32 and more, else 8.
+template <typename T>
+cudaError_t launch_ranges(const Params& q, bool prefix, bool own) {
+  return row_block(q.p, prefix ? q.p.all : q.p.rows) == 64 ? launch_range<T, 64, 64, 256>(q, prefix, own)
+                                                          : launch_range<T, 8, 64, 128>(q, prefix, own);
 }
 
 template <typename T>
@@ -449,7 +500,7 @@ cudaError_t launch_all(const Params& q) {
   if (q.p.mma) {
     e = launch_queries_mma(q);
   } else {
-    const size_t smem = (size_t)kPrepRows * (q.a.d + q.a.r) * 4;
+    const size_t smem = ((size_t)(kPrepRows + kPrepTile) * (q.a.d + 1) + kPrepTile * kPrepRows) * 4;
     queries_kernel<T><<<dim3((n + kPrepRows - 1) / kPrepRows + 1, q.a.H), 256, smem, q.a.stream>>>(q);
     e = cudaGetLastError();
   }
@@ -460,11 +511,11 @@ cudaError_t launch_all(const Params& q) {
     if (e == cudaSuccess) e = launch_ranges_mma(q);
     if (e != cudaSuccess) return e;
   } else {
-    for (int prefix = q.a.prefix_len > 0 ? 1 : 0; prefix >= 0; --prefix) {
-      const int rows = prefix ? q.p.all : q.p.rows;
-      e = rows >= 32 ? launch_range<T, 32, 32>(q, prefix != 0) : launch_range<T, 8, 64>(q, prefix != 0);
-      if (e != cudaSuccess) return e;
-    }
+    // one launch for the prefix and the own ranges where their row blocks are the same
+    const bool prefix = q.a.prefix_len > 0, both = row_block(q.p, q.p.all) == row_block(q.p, q.p.rows);
+    if (prefix && !both) e = launch_ranges<T>(q, true, false);
+    if (e == cudaSuccess) e = launch_ranges<T>(q, prefix && both, true);
+    if (e != cudaSuccess) return e;
   }
   const int64_t rows = (int64_t)q.a.Hk * q.p.all;
   // a warp a row while that gives every SM about eight warps
