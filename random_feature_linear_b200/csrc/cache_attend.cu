@@ -24,7 +24,7 @@ namespace cache {
 namespace {
 
 constexpr int kPrepRows = 8, kPrepTile = 32;         // (256 threads: one a row of M and query)
-constexpr long long kPrefixCtas = 4, kOwnCtas = 4;
+constexpr long long kPrefixCtas = 2, kOwnCtas = 4;
 
 // --------------------------------------------------- queries in fp32 (SIMT) --
 
@@ -447,7 +447,8 @@ Plan make_plan(const CacheAttnArgs& a) {
   const long long pb = (long long)a.Hk * ((p.all + prb - 1) / prb);
   const int steps = (a.prefix_len + kKeyStep - 1) / kKeyStep;
   long long s = (want + pb - 1) / pb;
-  if (s > (steps + 1) / 2) s = (steps + 1) / 2;
+  const long long most = p.mma ? (steps + 1) / 2 : steps;
+  if (s > most) s = most;
   if (s < 1) s = 1;
   p.p_chunk = steps == 0 ? kKeyStep : (int)((steps + s - 1) / s * kKeyStep);
   p.p_splits = steps == 0 ? 1 : (a.prefix_len + p.p_chunk - 1) / p.p_chunk;
