@@ -23,7 +23,7 @@
 namespace dark {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;   // of the backward pass
+constexpr int kMaxThreads = 256;                        // of the backward pass
 constexpr int kRowWarps = 4;                            // of the forward pass
 
 // A run of N elements of T as raw words, loaded and stored at once (2 to 16 bytes).
@@ -378,40 +378,50 @@ struct PartRows {
   int64_t first;                          // of the set
   int rows, group;                        // rows of one output row; the set's first head group
 };
-__device__ __forceinline__ int head_split(int nh) { return nh < kWarps ? kWarps / nh : 1; }
+// Warps of a CTA: eight, or for more heads the count from five up that leaves the fewest of
+// the groups' warps without a head.
+__host__ __device__ inline int bwd_warps(int nh) {
+  int best = 8;
+  for (int w = 7; w >= 5 && nh > 8; --w)
+    if ((nh + w - 1) / w * w < (nh + best - 1) / best * best) best = w;
+  return best;
+}
+__host__ __device__ inline int head_split(int nh) { return nh < 8 ? 8 / nh : 1; }
 __device__ __forceinline__ PartRows part_rows(const NormRopeArgs& a, int set, int ctas) {
   const int h0 = a.set[0].heads, nh = h0 + a.set[1].heads;
   const int lo = set ? h0 : 0, hi = set ? nh : h0;
   PartRows p;
   p.first = set ? (int64_t)h0 * ctas * head_split(nh) : 0;
-  p.group = lo / kWarps;
-  p.rows = a.set[set].gheads > 1 ? ctas * head_split(nh) : ((hi - 1) / kWarps - p.group + 1) * ctas;
+  const int w = bwd_warps(nh);
+  p.group = lo / w;
+  p.rows = a.set[set].gheads > 1 ? ctas * head_split(nh) : ((hi - 1) / w - p.group + 1) * ctas;
   return p;
 }
 
-// Backward. blockIdx.y is a group of at most kWarps heads, a warp keeps one head (with
-// fewer heads, several warps share one and split its tokens) and its weights and dgamma
+// Backward. blockIdx.y is a group of as many heads as the CTA has warps, a warp keeps one
+// head (with fewer heads, several warps share one and split its tokens) and its weights and dgamma
 // in registers. A CTA walks its `span` tokens; the rows of its warps stream through S slots
 // of shared memory a lane, and the cosines and sines of `tile` tokens at a time lie in
 // shared memory for all its heads: pairs 2 j, 2 j + 1 of unit u of token k as one float4
 // (two cosines, two sines) at (j tile + k) units + u, so that the lanes of a warp read
 // consecutive 16-byte words. Each warp leaves one row of sums for the reduction below.
 template <typename T, int N, int NU, int S, bool INTER>
-__global__ void __launch_bounds__(kThreads, 2) rows_bwd_kernel(const __grid_constant__ NormRopeArgs a,
+__global__ void __launch_bounds__(kMaxThreads, 2) rows_bwd_kernel(const __grid_constant__ NormRopeArgs a,
                                                                int lanes, int span, int tile) {
   using R = Run<T, N>;
   constexpr int NC = N > 1 ? N / 2 : 1, PC = N > 1 ? 2 : 1;
   constexpr uint32_t kRun = 32 * R::kBytes, kStage = NU * 4 * kRun;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ uint64_t turns[128];
-  float* cs = reinterpret_cast<float*>(smem + kWarps * S * kStage);
+  const int nw = blockDim.x / 32;
+  float* cs = reinterpret_cast<float*>(smem + nw * S * kStage);
   pdl_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rows = 32 / lanes, g = lane / lanes, lu = lane % lanes;
   const int np = a.rope.dims / 2, units = np / N;
   const int nh = a.set[0].heads + a.set[1].heads;
-  const int hg = nh < kWarps ? nh : kWarps, split = kWarps / hg;
-  const int hh = blockIdx.y * kWarps + warp % hg, part = warp / hg;
+  const int hg = nh < nw ? nh : nw, split = nw / hg;
+  const int hh = blockIdx.y * nw + warp % hg, part = warp / hg;
   const bool on = hh < nh && part < split;
   const int which = hh >= a.set[0].heads ? 1 : 0;
   const RowSet& rs = a.set[which];
@@ -488,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 2) rows_bwd_kernel(const __grid_cons
   for (int tile0 = 0; tile0 < count; tile0 += tile) {
     const int here = min(tile, count - tile0);
     __syncthreads();                                 // turns; the last tile's readers are done
-    for (int kk = warp; kk < here; kk += kWarps) {
+    for (int kk = warp; kk < here; kk += nw) {
       const uint32_t n = t0 + tile0 + kk;
       const int64_t pos = a.positions != nullptr ? (int64_t)a.positions[n] : a.pos0 + n % a.L;
       for (int p = lane; p < np; p += 32) {
@@ -598,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 2) rows_bwd_kernel(const __grid_cons
     }
   __syncthreads();
   // one partial row for every set with a shared weight, or one for every head
-  for (int c = threadIdx.x; c < a.d; c += kThreads)
+  for (int c = threadIdx.x; c < a.d; c += blockDim.x)
     for (int s = 0; s < 2; ++s) {
       const RowSet& r = a.set[s];
       if (r.gamma == nullptr) continue;
@@ -606,8 +616,8 @@ __global__ void __launch_bounds__(kThreads, 2) rows_bwd_kernel(const __grid_cons
       const int base = s ? a.set[0].heads : 0;
       float v = 0.f;
       bool any = false;
-      for (int i = 0; i < kWarps; ++i) {
-        const int hi = blockIdx.y * kWarps + i % hg, p = i / hg;
+      for (int i = 0; i < nw; ++i) {
+        const int hi = blockIdx.y * nw + i % hg, p = i / hg;
         if (hi >= nh || p >= split || hi < base || hi >= base + r.heads) continue;
         any = true;
         v += sums[i * a.d + c];
@@ -707,15 +717,14 @@ cudaError_t launch_rows(const NormRopeArgs& a) {
   return cudaGetLastError();
 }
 
-// CTAs along the tokens of the backward pass: two an SM over all head groups, and 16
-// tokens each at least.
+// CTAs along the tokens of the backward pass: as many over all head groups as run at once
+// (16 warps an SM by their registers), and 16 tokens each at least. The workspace follows
+// them, so that they are counted for the B200's 148 SMs.
 int bwd_ctas(int64_t ntok, int nh) {
-  const int groups = (nh + kWarps - 1) / kWarps;
+  const int w = bwd_warps(nh), groups = (nh + w - 1) / w, most = 148 * (16 / w) / groups;
   const int64_t least = (ntok + 15) / 16;
-  const int64_t most = 296 / groups > 0 ? 296 / groups : 1;
-  return (int)(least < most ? least : most);
+  return (int)(least < most ? least : most > 1 ? most : 1);
 }
-int bwd_split(int nh) { return nh < kWarps ? kWarps / nh : 1; }
 
 template <typename T, int N, bool INTER>
 cudaError_t launch_rows_bwd(const NormRopeArgs& a) {
@@ -724,18 +733,18 @@ cudaError_t launch_rows_bwd(const NormRopeArgs& a) {
   const int lanes = lanes_for(a.d, N);
   const int nh = a.set[0].heads + a.set[1].heads, np = a.rope.dims / 2;
   const int64_t ntok = (int64_t)a.B * a.L;
-  const int ctas = bwd_ctas(ntok, nh), step = 32 / lanes * bwd_split(nh);
+  const int ctas = bwd_ctas(ntok, nh), step = 32 / lanes * head_split(nh);
   const int span = (int)((ntok + ctas - 1) / ctas);
-  // angles of at most 32 KB at a time; tiles a multiple of the tokens of one step
-  const int most = (np == 0 ? span : 4096 / np) / step * step;
+  // angles of at most 48 KB at a time; tiles a multiple of the tokens of one step
+  const int most = (np == 0 ? span : 6144 / np) / step * step, nw = bwd_warps(nh);
   const int tile = most < step ? step : most < span ? most : (span + step - 1) / step * step;
-  const size_t ring = (size_t)kWarps * S * NU * 4 * 32 * N * sizeof(T);
+  const size_t ring = (size_t)nw * S * NU * 4 * 32 * N * sizeof(T);
   const size_t smem = ring + (size_t)tile * a.rope.dims * sizeof(float);
   auto* kernel = rows_bwd_kernel<T, N, NU, S, INTER>;
-  cudaError_t e = set_smem_limit_once((const void*)kernel, (int)(ring + 65536), smem_set);
+  cudaError_t e = set_smem_limit_once((const void*)kernel, (int)(ring + 49152), smem_set);
   if (e != cudaSuccess) return e;
-  const dim3 grid(ctas, (nh + kWarps - 1) / kWarps);
-  kernel<<<grid, kThreads, smem, a.stream>>>(a, lanes, span, tile);
+  const dim3 grid(ctas, (nh + nw - 1) / nw);
+  kernel<<<grid, 32 * nw, smem, a.stream>>>(a, lanes, span, tile);
   e = cudaGetLastError();
   const int out_rows = (a.set[0].gamma ? a.set[0].gheads : 0) + (a.set[1].gamma ? a.set[1].gheads : 0);
   if (e != cudaSuccess || out_rows == 0) return e;
@@ -743,10 +752,13 @@ cudaError_t launch_rows_bwd(const NormRopeArgs& a) {
 }
 
 // The instance for a call's type, unit width and pair layout.
+// (The backward pass holds four rows' worth of a unit in registers: units of four pairs at
+// most, 77 us against 88 with eight at 16384 tokens of 20 heads, d = 128, bf16.)
 template <typename T, int N>
 cudaError_t launch_n(const NormRopeArgs& a, bool bwd) {
-  if (a.rope.interleaved) return bwd ? launch_rows_bwd<T, N, true>(a) : launch_rows<T, N, true>(a);
-  return bwd ? launch_rows_bwd<T, N, false>(a) : launch_rows<T, N, false>(a);
+  constexpr int NB = N > 4 ? 4 : N;
+  if (a.rope.interleaved) return bwd ? launch_rows_bwd<T, NB, true>(a) : launch_rows<T, N, true>(a);
+  return bwd ? launch_rows_bwd<T, NB, false>(a) : launch_rows<T, N, false>(a);
 }
 cudaError_t launch(const NormRopeArgs& a, bool bwd) {
   const int n = pairs_for(a);
@@ -764,7 +776,7 @@ cudaError_t launch(const NormRopeArgs& a, bool bwd) {
 
 size_t norm_rope_bwd_workspace_bytes(int B, int H, int Hk, int L, int d) {
   const int nh = H + Hk;
-  return kWsHeader + align_up((size_t)nh * bwd_ctas((int64_t)B * L, nh) * bwd_split(nh) * d * 4, 256);
+  return kWsHeader + align_up((size_t)nh * bwd_ctas((int64_t)B * L, nh) * head_split(nh) * d * 4, 256);
 }
 
 cudaError_t launch_norm_rope(const NormRopeArgs& a) { return launch(a, false); }
