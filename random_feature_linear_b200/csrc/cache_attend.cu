@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Param
 // -------------------------------------------------------------------- the plan --
 
 int row_block(const Plan& p, int rows) {
-  if (p.mma) return mma_rows(p.rows);
+  if (p.mma) return mma_rows(p.dp, p.rows);
   return rows >= 32 ? 64 : 8;
 }
 
@@ -443,7 +443,7 @@ Plan make_plan(const CacheAttnArgs& a) {
   p.share = p.mma && !p.tc && p.all > 16 && a.prefix_len > 0;
   // ranges: about as many CTAs (over key heads, row blocks and ranges) as run at once
   const long long want = kPrefixCtas * 148, want_own = kOwnCtas * 148;
-  const int prb = p.share ? share_rows(p.all) : row_block(p, p.all);
+  const int prb = p.share ? share_rows(p.dp, p.all) : row_block(p, p.all);
   const long long pb = (long long)a.Hk * ((p.all + prb - 1) / prb);
   const int steps = (a.prefix_len + kKeyStep - 1) / kKeyStep;
   long long s = (want + pb - 1) / pb;

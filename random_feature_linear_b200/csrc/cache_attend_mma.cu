@@ -11,9 +11,9 @@
 // mma.sync m16n8k16 has 16 rows. Eight queries fill it twice, as y = hi + lo: rows 0-7 hold
 // hi, rows 8-15 lo, and a thread's accumulators of rows g and g + 8 add up to the score; the
 // weights P = hi + lo go the same way, so that both products keep 16 bits of significand at
-// the price of one product with 16 rows. With more rows the tile holds 16 queries and
-// weights rounded to bf16 (twice the products for hi + lo made the 16-row case slower by a
-// third). A row's reference exponent only moves when a score passes it by 2^8 (sums and
+// the price of one product with 16 rows. With more rows, up to d = 128, the tile holds 16
+// queries, hi and lo in two products, and weights rounded to bf16 (8-row tiles cost a
+// quarter more at 16 rows). A row's reference exponent only moves when a score passes it by 2^8 (sums and
 // weights stay far inside fp32), so that sums are rescaled a few times a range.
 //
 // Bound by the key and value rows (read once for all rows of the block): 4 d bytes a key;
@@ -161,8 +161,10 @@ __global__ void __launch_bounds__(Cfg<DP, SHARE>::W * 32) range_mma_kernel(const
     }
   }
 
-  // the rows' queries as A fragments: hi in rows 0-7 and lo in rows 8-15, or rows 0-15
-  uint32_t ya[NS][4];
+  // the rows' queries as A fragments: hi in rows 0-7 and lo in rows 8-15, or rows 0-15 of
+  // hi, then of lo
+  constexpr int NH = HL ? 1 : 2;
+  uint32_t ya[NH][NS][4];
   int lim[NR], seen_by_all = it.k1;
   {
     const __nv_bfloat16* y = at<__nv_bfloat16>(q.a, q.p.o_y);
@@ -180,10 +182,13 @@ __global__ void __launch_bounds__(Cfg<DP, SHARE>::W * 32) range_mma_kernel(const
       }
     }
 #pragma unroll
-    for (int s = 0; s < NS; ++s)
+    for (int h = 0; h < NH; ++h)
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        ya[s][e] = ok[e & 1] ? __ldcg(reinterpret_cast<const uint32_t*>(src[e & 1] + 16 * s + 8 * (e >> 1))) : 0u;
+      for (int s = 0; s < NS; ++s)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          ya[h][s][e] = ok[e & 1] ? __ldcg(reinterpret_cast<const uint32_t*>(src[e & 1] + h * lo + 16 * s + 8 * (e >> 1)))
+                                  : 0u;
     for (int o = 4; o < 32; o <<= 1)
       seen_by_all = min(seen_by_all, __shfl_xor_sync(0xffffffffu, seen_by_all, o));
   }
@@ -220,8 +225,11 @@ __global__ void __launch_bounds__(Cfg<DP, SHARE>::W * 32) range_mma_kernel(const
       for (int kg = 0; kg < KG; ++kg) {
         uint32_t b[4];
         ldsm4(b, k0 + tile_off<DP>(kg * 16 + (lg >> 1) * 8 + lr, 2 * st + (lg & 1)));
-        mma16816_bf16(s[2 * kg], ya[st], b[0], b[1]);
-        mma16816_bf16(s[2 * kg + 1], ya[st], b[2], b[3]);
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          mma16816_bf16(s[2 * kg], ya[h][st], b[0], b[1]);
+          mma16816_bf16(s[2 * kg + 1], ya[h][st], b[2], b[3]);
+        }
       }
     const int tile0 = first_key(i), key0 = tile0 + 2 * t;
     uint32_t pa[KG][4];
@@ -380,21 +388,21 @@ cudaError_t launch(const Params& q, long long n) {
 }
 template <bool HL, bool SHARE>
 cudaError_t launch_dp(const Params& q, long long n) {
-  return q.p.dp == 64    ? launch<64, HL, SHARE>(q, n)
-         : q.p.dp == 128 ? launch<128, HL, SHARE>(q, n)
-                         : launch<256, HL, SHARE>(q, n);
+  if constexpr (HL)
+    if (q.p.dp == 256) return launch<256, HL, SHARE>(q, n);
+  return q.p.dp == 64 ? launch<64, HL, SHARE>(q, n) : launch<128, HL, SHARE>(q, n);
 }
 
 }  // namespace
 
 cudaError_t launch_prefix_mma(const Params& q) {
-  const int rb = share_rows(q.p.all);
+  const int rb = share_rows(q.p.dp, q.p.all);
   const long long n = (long long)q.p.p_splits * ((q.p.all + rb - 1) / rb);
-  return q.p.all <= 32 ? launch_dp<true, true>(q, n) : launch_dp<false, true>(q, n);
+  return rb == 32 ? launch_dp<true, true>(q, n) : launch_dp<false, true>(q, n);
 }
 
 cudaError_t launch_ranges_mma(const Params& q) {
-  const int rb = mma_rows(q.p.rows);
+  const int rb = mma_rows(q.p.dp, q.p.rows);
   long long n = (long long)q.p.cap * ((q.p.rows + rb - 1) / rb);
   if (q.a.prefix_len > 0 && !q.p.tc && !q.p.share) n += (long long)q.p.p_splits * ((q.p.all + rb - 1) / rb);
   return rb == 8 ? launch_dp<true, false>(q, n) : launch_dp<false, false>(q, n);

@@ -8,11 +8,11 @@ namespace dark {
 namespace cache {
 
 // Rows that one CTA of the tensor-core range kernel takes at once.
-inline int mma_rows(int rows) { return rows > 8 ? 16 : 8; }
+inline int mma_rows(int dp, int rows) { return dp <= 128 && rows > 8 ? 16 : 8; }
 cudaError_t launch_ranges_mma(const Params& q);
 
 // The prefix's ranges for more rows, which share the keys in a CTA.
-inline int share_rows(int all) { return all <= 32 ? 32 : 64; }
+inline int share_rows(int dp, int all) { return dp <= 128 && all > 32 ? 64 : 32; }
 cudaError_t launch_prefix_mma(const Params& q);
 
 // Rows of a block of the tcgen05 kernel (dp <= 128), keys of its tiles.

@@ -10,8 +10,10 @@
 // starts on the first 64 keys while the others are weighed. While one tile's scores are
 // exponentiated the other tile's products run.
 //
-// Queries and weights are rounded to bf16 (the products' operand type); scores, sums and
-// exponents are fp32. Whole tiles of keys and values come by tensor copies of as many rows as
+// Queries are hi + lo in bf16 (one bf16 alone doubled the error of the result: 3.7e-3 against
+// 1.7e-3 of its size at 32768 keys), so that the first product has two parts; weights are
+// rounded to bf16, a smaller error than the result's own rounding; scores, sums and exponents
+// are fp32. Whole tiles of keys and values come by tensor copies of as many rows as
 // divide both the page and the tile (8 at least); tiles that end inside the range's last page, and pages
 // of other sizes, by 16-byte asynchronous copies with zeros behind the end (stale rows of a
 // page may hold anything, and a weight of 0 does not cancel an infinity). Those take about
@@ -40,9 +42,10 @@ struct Tc {
   static constexpr int RT = 2;                        // row tiles (TMEM: RT (128 + DP) columns)
   static constexpr int kBlk = kT * 128;               // 128 rows of 64 columns
   static constexpr uint32_t kTile = DP / 64 * kBlk;   // 128 rows of DP columns, bf16
-  static constexpr int kSlots = 4;                    // ring of key and value tiles
-  static constexpr uint32_t oQ = 0, oRing = RT * kTile, oRows = oRing + kSlots * kTile;
-  static constexpr uint32_t oBar = oRows + 2 * kT * 8, kSmem = oBar + 256 + 1024;
+  static constexpr int kSlots = DP == 64 ? 4 : 3;     // ring of key and value tiles
+  // queries: hi of the row tiles, then lo
+  static constexpr uint32_t oQ = 0, oRing = 2 * RT * kTile, oRows = oRing + kSlots * kTile;
+  static constexpr uint32_t oBar = oRows + kT * 8, kSmem = oBar + 256 + 1024;
   static constexpr uint32_t tS = 0, tO = RT * 128, kCols = 512;
   static_assert(tO + RT * DP <= kCols, "tmem");
   static_assert(kSmem <= 232448, "shared memory");
@@ -214,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1) range_tc_kernel(const __grid_cons
                                                                 const __grid_constant__ CUtensorMap tm_v) {
   using C = Tc<DP>;
   constexpr int RT = C::RT, S = C::kSlots, CH = DP / 8;
-  static_assert(S >= 4 && S <= 8 && S % 2 == 0, "ring");
+  static_assert(S >= 3 && S <= 8, "ring");
   static_assert(sizeof(Bars) <= 256, "barriers");
   const int hk = blockIdx.y;
   const Item it = item_of(q, blockIdx.x, hk, RT * kT, true, false);
@@ -270,9 +273,13 @@ __global__ void __launch_bounds__(kThreads, 1) range_tc_kernel(const __grid_cons
     const bool in = c < 2 * ks, has = c * 8 < d;      // (a last half step is zeros)
     const int n = 2 * tiles, box = q.box_rows, nb = (d + 63) / 64;
     const __nv_bfloat16* y = at<__nv_bfloat16>(q.a, q.p.o_y) + ((int64_t)hk * q.p.all + it.row0) * DP;
-    for (int r = t / CH; r < rts * kT; r += kLoad / CH)
-      cp16(s0 + C::oQ + (r / kT) * C::kTile + kmajor_off(r % kT, c * 8, C::kBlk),
-           y + (r < it.nrows ? (int64_t)r * DP + c * 8 : 0), r < it.nrows);
+    const int64_t lo = (int64_t)q.a.Hk * q.p.all * DP;
+    for (int r = t / CH; r < rts * kT; r += kLoad / CH) {
+      const uint32_t to = s0 + C::oQ + (r / kT) * C::kTile + kmajor_off(r % kT, c * 8, C::kBlk);
+      const __nv_bfloat16* src = y + (r < it.nrows ? (int64_t)r * DP + c * 8 : 0);
+      cp16(to, src, r < it.nrows);
+      cp16(to + RT * C::kTile, src + lo, r < it.nrows);
+    }
     cp_commit();
     int64_t* rows = reinterpret_cast<int64_t*>(sm + C::oRows);
     int done = 0;                                     // copies handed over (this thread's part)
@@ -318,6 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1) range_tc_kernel(const __grid_cons
         continue;
       }
       if (!(i & 1)) {
+        loaders_sync_or(false);                       // the last tile's rows have been used
         for (int k = t; k < kT; k += kLoad) {
           const int key = key0 + k;
           int64_t row = -1;
@@ -325,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) range_tc_kernel(const __grid_cons
             row = cache_row(q.a, it.pages, key, hk);
             if (row < 0) report(status, DARK_ERR_INVALID_ARG);
           }
-          rows[(j & 1) * kT + k] = row;
+          rows[k] = row;
         }
         ok = !loaders_sync_or(!ok);
       }
@@ -333,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1) range_tc_kernel(const __grid_cons
         const __nv_bfloat16* pool = (const __nv_bfloat16*)(i & 1 ? q.a.vp : q.a.kp) + c * 8;
 #pragma unroll 4
         for (int r = t / CH; r < kT; r += kLoad / CH) {
-          const int64_t row = rows[(j & 1) * kT + r];
+          const int64_t row = rows[r];
           const bool live = row >= 0 && has;
           cp16(dst + kmajor_off(r, c * 8, C::kBlk), pool + (live ? row * d : 0), live);
         }
@@ -365,11 +373,13 @@ __global__ void __launch_bounds__(kThreads, 1) range_tc_kernel(const __grid_cons
         if (!lead) return;
         const uint64_t a = dq + (uint32_t)(x * (C::kTile >> 4)), b = dk + (uint32_t)(i % S * (C::kTile >> 4));
 #pragma unroll
-        for (int s = 0; s < DP / 16; ++s)
-          if (s < ks) {
-            const uint32_t step = (s / 4 * C::kBlk + s % 4 * 32) >> 4;
-            mma(tmem + C::tS + x * kT, a + step, b + step, id_s, s > 0);
-          }
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int s = 0; s < DP / 16; ++s)
+            if (s < ks) {
+              const uint32_t step = (s / 4 * C::kBlk + s % 4 * 32) >> 4;
+              mma(tmem + C::tS + x * kT, a + h * (RT * C::kTile >> 4) + step, b + step, id_s, h + s > 0);
+            }
         mma_commit(&bar->s[x]);
         if (x == rts - 1) mma_commit(&bar->empty[i % S]);
       };
