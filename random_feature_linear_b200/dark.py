@@ -9,7 +9,6 @@ module fails loudly if that library has not been built.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 
 import torch
@@ -403,29 +402,46 @@ def dark_sample_omega(seed: int, draw: int, omega, orthogonal: bool = True, ws=N
 # These calls take their sizes from the tensors, so the binding checks that the
 # tensors agree; what the C ABI checks (ranges, alignment, flags) stays there.
 
+# torch.cuda.current_stream and current_device without their Python layers
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _DTYPES = {torch.float32: DARK_F32, torch.bfloat16: DARK_BF16}
 
 
-@functools.lru_cache(maxsize=4096)
-def _s3(b, h, l):
-    """Element strides {b, h, l} as the C ABI takes them (read-only there)."""
-    return (ctypes.c_int64 * 3)(b, h, l)
+_stride_arrays = {}
 
 
-def _rows(t, name, B, L, d, dtype, dev):
-    """A [B][heads][L][d] tensor with a unit d stride: pointer, strides, heads."""
-    n, s = t.shape, t.stride()
-    if len(n) != 4 or n[0] != B or n[2] != L or n[3] != d:
-        raise ValueError(f"{name}: expected [B][heads][L][d] = [{B}][..][{L}][{d}]")
-    if s[3] != 1 or t.dtype is not dtype or t.get_device() != dev:
-        raise ValueError(f"{name}: expected type {dtype} and a unit d stride, on q's device")
-    return t.data_ptr(), _s3(s[0], s[1], s[2]), n[1]
+def _s3(strides):
+    """Element strides {b, h, l} as the C ABI takes them (read-only there; the arrays, a few for
+    every layout in use, are kept)."""
+    a = _stride_arrays.get(strides)
+    if a is None:
+        if len(_stride_arrays) >= 4096:
+            _stride_arrays.clear()
+        a = _stride_arrays[strides] = (ctypes.c_int64 * 3)(*strides[:3])
+    return a
+
+
+def _rows(t, name, shape, dtype, dev):
+    """Pointer and strides of a tensor [B][heads][L][d] of the given shape with a unit d stride."""
+    s = t.stride()
+    if t.shape != shape or s[3] != 1 or t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError(f"{name}: expected a tensor of shape {tuple(shape)} ([B][heads][L][d]) and "
+                         f"type {dtype} with a unit d stride, on the same device")
+    return t.data_ptr(), _s3(s)
+
+
+def _like(t, name, first):
+    """The shape of a [B][heads][L][d] tensor whose head count may differ from `first`'s."""
+    n = t.shape
+    if len(n) != 4 or n[0] != first[0] or n[2] != first[2] or n[3] != first[3]:
+        raise ValueError(f"{name}: expected [B][heads][L][d] = [{first[0]}][..][{first[2]}][{first[3]}]")
+    return n
 
 
 def _want(t, name, shape, dtype, dev):
-    """The address of a dense tensor of the given shape, type and device; None: NULL."""
-    if t is None:
-        return None
+    """The address of a dense tensor of the given shape, type and device."""
     if t.shape != shape or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous tensor of shape {tuple(shape)} and type "
                          f"{dtype}, on the same device")
@@ -446,11 +462,12 @@ def _weight(g, name, heads, d, dev):
 
 
 def _first(t, name):
-    """Sizes, type code and device of the tensor that the others are held against."""
-    n, code = t.shape, _DTYPES.get(t.dtype)
+    """Shape, type and device of the tensor that the others are held against."""
+    n, dt = t.shape, t.dtype
+    code = _DTYPES.get(dt)
     if len(n) != 4 or code is None:
         raise ValueError(f"{name}: expected a [B][heads][L][d] tensor of fp32 or bf16")
-    return n[0], n[2], n[3], t.dtype, code, t.get_device()
+    return n, dt, code, t.get_device()
 
 
 def _bytes(ws, dev):
@@ -469,8 +486,8 @@ def _call(fn, dev, dev_status, stream, *args):
     if dev_status is not None and (dev_status.get_device() != dev
                                    or dev_status.dtype is not torch.int32):
         raise ValueError("dev_status: expected an int32 tensor on the same device")
-    stream = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
-    if torch._C._cuda_getDevice() == dev:
+    stream = _raw_stream(dev) if stream is None else _stream(stream)
+    if _current_device() == dev:
         status = fn(*args, _ptr(dev_status), stream)
     else:
         with torch.cuda.device(dev):
@@ -492,23 +509,25 @@ def dark_qk_norm_rope_fwd(q, k, q_out, k_out, gamma_q=None, gamma_k=None, eps: f
                           dev_status=None, stream=None) -> None:
     """Norms the head rows of q [B][H][L][d] and k [B][Hk][L][d] (k and k_out may be None)
     and rotates them by their positions (int32 [B][L], or None: pos0 + l)."""
-    B, L, d, dt, code, dev = _first(q, "q")
-    qp, qs, H = _rows(q, "q", B, L, d, dt, dev)
-    op, os_, n = _rows(q_out, "q_out", B, L, d, dt, dev)
+    nq, dt, code, dev = _first(q, "q")
+    B, H, L, d = nq
+    qp, qs = _rows(q, "q", nq, dt, dev)
+    op, os_ = _rows(q_out, "q_out", nq, dt, dev)
     kp = ks = kop = kos = None
-    Hk = nk = 0
+    Hk = 0
     if k is not None and k_out is not None:
-        kp, ks, Hk = _rows(k, "k", B, L, d, dt, dev)
-        kop, kos, nk = _rows(k_out, "k_out", B, L, d, dt, dev)
+        nk = _like(k, "k", nq)
+        Hk = nk[1]
+        kp, ks = _rows(k, "k", nk, dt, dev)
+        kop, kos = _rows(k_out, "k_out", nk, dt, dev)
     elif k is not k_out:
         raise ValueError("k and k_out: both or neither")
-    if n != H or nk != Hk:
-        raise ValueError("results have other head counts than their inputs")
     gq, hq = _weight(gamma_q, "gamma_q", H, d, dev)
     gk, hk = _weight(gamma_k, "gamma_k", Hk, d, dev)
+    pp = None if positions is None else _want(positions, "positions", (B, L), torch.int32, dev)
     _call(_lib.dark_qk_norm_rope_fwd, dev, dev_status, stream, qp, qs, kp, ks, op, os_, kop, kos,
-          gq, hq, gk, hk, eps, rope, _want(positions, "positions", (B, L), torch.int32, dev), pos0,
-          B, H, Hk, L, d, code)
+          gq, hq, gk, hk, eps, rope, pp, pos0, B, H, Hk, L, d,
+          code)
 
 
 def dark_qk_norm_rope_bwd_workspace_bytes(B: int, H: int, Hk: int, L: int, d: int) -> int:
@@ -527,30 +546,31 @@ def dark_qk_norm_rope_bwd(q, k, dq_out, dk_out, dq, dk, gamma_q=None, gamma_k=No
                           dev_status=None, stream=None) -> None:
     """Gradients of dark_qk_norm_rope_fwd: dq, dk of the inputs' type and dgamma_q,
     dgamma_k (fp32, of the weights' shape). ws: see alloc_qk_norm_rope_bwd_workspace."""
-    B, L, d, dt, code, dev = _first(q, "q")
-    qp, qs, H = _rows(q, "q", B, L, d, dt, dev)
-    gp, gs, n1 = _rows(dq_out, "dq_out", B, L, d, dt, dev)
-    op, os_, n2 = _rows(dq, "dq", B, L, d, dt, dev)
+    nq, dt, code, dev = _first(q, "q")
+    B, H, L, d = nq
+    qp, qs = _rows(q, "q", nq, dt, dev)
+    gp, gs = _rows(dq_out, "dq_out", nq, dt, dev)
+    op, os_ = _rows(dq, "dq", nq, dt, dev)
     kp = ks = kgp = kgs = kop = kos = None
-    Hk = n3 = n4 = 0
+    Hk = 0
     if k is not None and dk_out is not None and dk is not None:
-        kp, ks, Hk = _rows(k, "k", B, L, d, dt, dev)
-        kgp, kgs, n3 = _rows(dk_out, "dk_out", B, L, d, dt, dev)
-        kop, kos, n4 = _rows(dk, "dk", B, L, d, dt, dev)
+        nk = _like(k, "k", nq)
+        Hk = nk[1]
+        kp, ks = _rows(k, "k", nk, dt, dev)
+        kgp, kgs = _rows(dk_out, "dk_out", nk, dt, dev)
+        kop, kos = _rows(dk, "dk", nk, dt, dev)
     elif k is not None or dk_out is not None or dk is not None:
         raise ValueError("k, dk_out and dk: all or none")
-    if n1 != H or n2 != H or n3 != Hk or n4 != Hk:
-        raise ValueError("gradients have other head counts than their inputs")
     gq, hq = _weight(gamma_q, "gamma_q", H, d, dev)
     gk, hk = _weight(gamma_k, "gamma_k", Hk, d, dev)
     dgq, hdq = _weight(dgamma_q, "dgamma_q", H, d, dev)
     dgk, hdk = _weight(dgamma_k, "dgamma_k", Hk, d, dev)
     if (gq and dgq and hdq != hq) or (gk and dgk and hdk != hk):
         raise ValueError("a weight's gradient has the weight's shape")
+    pp = None if positions is None else _want(positions, "positions", (B, L), torch.int32, dev)
     _call(_lib.dark_qk_norm_rope_bwd, dev, dev_status, stream, qp, qs, kp, ks, gp, gs, kgp, kgs,
           op, os_, kop, kos, gq, hq, gk, hk, dgq, dgk, eps, rope,
-          _want(positions, "positions", (B, L), torch.int32, dev), pos0, B, H, Hk, L, d, code,
-          *_bytes(ws, dev))
+          pp, pos0, B, H, Hk, L, d, code, *_bytes(ws, dev))
 
 
 def kv_cache(k_pages, v_pages) -> dark_kv_cache:
@@ -580,17 +600,19 @@ def dark_kv_append(cache: dark_kv_cache, k, v, page_table, lens, new_lens=None, 
     """Appends k, v [B][heads][T][d] behind the lens[b] tokens of every sequence, the keys
     normed and rotated on the way. page_table int32 [B][max_pages], lens int32 [B], new_lens
     int32 [B] (None: all T), positions int32 [B][T] (None: pos0 + lens[b] + t)."""
-    B, T, d, dt, code, dev = _first(k, "k")
-    kp, ks, n1 = _rows(k, "k", B, T, d, dt, dev)
-    vp, vs, n2 = _rows(v, "v", B, T, d, dt, dev)
-    if n1 != cache.heads or n2 != n1 or d != cache.d or code != cache.dtype \
+    n, dt, code, dev = _first(k, "k")
+    B, Hk, T, d = n
+    kp, ks = _rows(k, "k", n, dt, dev)
+    vp, vs = _rows(v, "v", n, dt, dev)
+    if Hk != cache.heads or d != cache.d or code != cache.dtype \
             or cache.device not in (None, dev):
         raise ValueError("k, v: expected the cache's heads, d, type and device")
     tp, max_pages, lp = _lists(page_table, lens, B, dev)
-    g, hg = _weight(gamma_k, "gamma_k", n1, d, dev)
-    _call(_lib.dark_kv_append, dev, dev_status, stream, cache, kp, ks, vp, vs, B, T, tp, max_pages,
-          lp, _want(new_lens, "new_lens", (B,), torch.int32, dev), g, hg, eps, rope,
-          _want(positions, "positions", (B, T), torch.int32, dev), pos0)
+    g, hg = _weight(gamma_k, "gamma_k", Hk, d, dev)
+    nl = None if new_lens is None else _want(new_lens, "new_lens", (B,), torch.int32, dev)
+    pp = None if positions is None else _want(positions, "positions", (B, T), torch.int32, dev)
+    _call(_lib.dark_kv_append, dev, dev_status, stream, cache, kp, ks, vp, vs, B, T, tp,
+          max_pages, lp, nl, g, hg, eps, rope, pp, pos0)
 
 
 def dark_cache_attention_workspace_bytes(proj: dark_projection, cache: dark_kv_cache, B: int,
@@ -611,12 +633,12 @@ def dark_cache_attention_fwd(proj: dark_projection, cache: dark_kv_cache, q, out
     """Exact-mode attention of q [B][H][T][d] over the shared prefix (prefix_pages int32
     [ceil(prefix_len / page_size)]) and each sequence's lens[b] own tokens. ws: see
     alloc_cache_attention_workspace."""
-    B, T, d, dt, code, dev = _first(q, "q")
-    qp, qs, H = _rows(q, "q", B, T, d, dt, dev)
-    op, os_, n = _rows(out, "out", B, T, d, dt, dev)
-    if n != H or d != cache.d or code != cache.dtype \
-            or cache.device not in (None, dev):
-        raise ValueError("q, out: expected equal head counts and the cache's d, type and device")
+    n, dt, code, dev = _first(q, "q")
+    B, H, T, d = n
+    qp, qs = _rows(q, "q", n, dt, dev)
+    op, os_ = _rows(out, "out", n, dt, dev)
+    if d != cache.d or code != cache.dtype or cache.device not in (None, dev):
+        raise ValueError("q, out: expected the cache's d, type and device")
     tp, max_pages, lp = _lists(page_table, lens, B, dev)
     xp = None
     if prefix_len > 0 and prefix_pages is not None:
@@ -624,8 +646,9 @@ def dark_cache_attention_fwd(proj: dark_projection, cache: dark_kv_cache, q, out
         if len(n) != 1 or n[0] * cache.page_size < prefix_len:
             raise ValueError("prefix_pages: expected int32 [ceil(prefix_len / page_size)]")
         xp = _want(prefix_pages, "prefix_pages", n, torch.int32, dev)
-    _call(_lib.dark_cache_attention_fwd, dev, dev_status, stream, proj, cache, qp, qs, op, os_, B,
-          H, T, xp, prefix_len, tp, max_pages, lp, flags, *_bytes(ws, dev))
+    wp, wn = _bytes(ws, dev)
+    _call(_lib.dark_cache_attention_fwd, dev, dev_status, stream, proj, cache, qp, qs, op,
+          os_, B, H, T, xp, prefix_len, tp, max_pages, lp, flags, wp, wn)
 
 
 class RedrawSchedule:

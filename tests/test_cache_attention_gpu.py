@@ -340,6 +340,33 @@ def test_bad_lists_are_reported(D, cuda_ok, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F])
+def test_lists_may_share_pages(D, cuda_ok, dtype):
+    """Sequences with the same pages, and a prefix that is also a sequence's own."""
+    c = Call(D, dtype=dtype, B=3, T=2, prefix=64, lens=(40, 40, 40), page=16)
+    c.table[1] = c.table[0]
+    c.table[2] = c.shared[:3]
+    c.kp.nan_to_num_(0.5), c.vp.nan_to_num_(0.5, posinf=0.25)
+    c.d_table.copy_(_i32(c.table))
+    c.run()
+    c.check()
+    q = c.q.clone()
+    q[1] = q[0]
+    c.q = q
+    c.run()
+    assert torch.equal(c.out[0], c.out[1])
+
+
+def test_queries_past_fp16_are_reported(D, cuda_ok):
+    c = Call(D, prefix=20)
+    c.q[1, 2, 0, 5] = 1e5
+    c.run()
+    assert c.status.item() == D.DARK_ERR_NUMERIC
+    rest = torch.ones(2, 4, dtype=torch.bool)
+    rest[1, 2] = False
+    assert torch.isfinite(c.out[rest.cuda()]).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
 def test_calls_repeat_to_the_bit_and_share_no_state(D, cuda_ok, dtype):
     """Again, in a replayed graph on another stream, and two calls at once."""
     a = Call(D, dtype=dtype, B=9, H=8, T=2, prefix=300, lens=tuple(range(0, 90, 10)), causal=True)

@@ -234,6 +234,50 @@ def test_zero_rows(D, cuda_ok):
     assert not dg.any()
 
 
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_captured_calls_replay(D, cuda_ok, dtype):
+    """Norm, gradient and append captured into one graph, replayed on new contents."""
+    rng = np.random.default_rng(7)
+    B, H, L, d, page = 3, 4, 20, 64, 16
+    q, k, v, dq, dk = (_t(rng, B, H, L, d, dtype=dtype) for _ in range(5))
+    gamma = 1 + 0.1 * _t(rng, H, d)
+    rope = D.dark_rope_init(d)
+    new = lambda t: torch.full_like(t, float("nan"))
+    outs = [new(q), new(k), new(q), new(k), new(gamma), new(gamma)]
+    table = torch.arange(B * 3, dtype=torch.int32, device="cuda").reshape(B, 3)
+    lens = torch.tensor([0, 5, 17], dtype=torch.int32, device="cuda")
+    kp, vp = (torch.zeros(B * 3, H, page, d, dtype=dtype, device="cuda") for _ in range(2))
+    cache = D.kv_cache(kp, vp)
+    ws = D.alloc_qk_norm_rope_bwd_workspace(B, H, H, L, d, "cuda")
+
+    def step():
+        D.dark_qk_norm_rope_fwd(q, k, outs[0], outs[1], gamma_q=gamma, gamma_k=gamma, rope=rope)
+        D.dark_qk_norm_rope_bwd(q, k, dq, dk, outs[2], outs[3], gamma_q=gamma, gamma_k=gamma,
+                                dgamma_q=outs[4], dgamma_k=outs[5], rope=rope, ws=ws)
+        D.dark_kv_append(cache, k, v, table, lens, gamma_k=gamma, rope=rope)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for t in (q, k, v, dq, dk):
+        t.copy_(_t(rng, B, H, L, d, dtype=dtype))
+    lens.add_(2)
+    step()
+    want = [t.clone() for t in outs + [kp, vp]]
+    for t in outs + [kp, vp]:
+        t.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(outs, want):
+        assert torch.equal(a, b)
+    for b in range(B):                                # places that this append writes
+        for j in range(int(lens[b]), int(lens[b]) + L):
+            p = int(table[b, j // page])
+            assert torch.equal(kp[p, :, j % page], want[6][p, :, j % page])
+            assert torch.equal(vp[p, :, j % page], want[7][p, :, j % page])
+
+
 # ----------------------------------------------------------------- append --
 
 # dtype, B, Hk, T, d, rot, interleaved, weight, page, have (per sequence), new, packed
