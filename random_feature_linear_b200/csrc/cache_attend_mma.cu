@@ -2,7 +2,7 @@
 //
 // A CTA takes one key range and a block of rows, in one of two ways:
 //  * few rows (a sequence's own keys; a prefix with up to 16 rows): every warp streams its
-//    own tiles of 16 or 32 keys (tiles w, w + warps, ...) through a private ring in shared
+//    own tiles of 16 keys (tiles w, w + warps, ...) through a private ring in shared
 //    memory (cp.async, 16 bytes a lane, no barrier between warps) for the same 8 or 16 rows,
 //    and keeps its own reference exponents, weights and sums, joined once at the end;
 //  * a prefix with more rows: all warps share each tile of keys, brought by all of them, and
@@ -27,6 +27,8 @@ namespace dark {
 namespace cache {
 namespace {
 
+constexpr int kKeys = 16;                                 // keys of a tile
+
 
 __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
   uint32_t v;
@@ -36,11 +38,11 @@ __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
 __device__ __forceinline__ float bf16_half(uint32_t w, int upper) {
   return __uint_as_float(upper ? w & 0xffff0000u : w << 16);
 }
-// Whether a tile of KEYS rows holds an infinity or NaN (the same answer in all lanes).
-template <int DP, int KEYS>
+// Whether a tile of kKeys rows holds an infinity or NaN (the same answer in all lanes).
+template <int DP>
 __device__ __forceinline__ bool tile_non_finite(uint32_t tile, int lane) {
   bool bad = false;
-  for (int n = lane; n < KEYS * DP / 8; n += 32) {
+  for (int n = lane; n < kKeys * DP / 8; n += 32) {
     const uint4 w = tc::ld_shared_v4(tile + 16 * n);
     for (uint32_t x : {w.x, w.y, w.z, w.w})
       bad |= (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
@@ -49,13 +51,14 @@ __device__ __forceinline__ bool tile_non_finite(uint32_t tile, int lane) {
 }
 
 // Shared memory of a CTA: rings of `kStages` tiles for each of W warps, or one for all.
-// Two CTAs an SM, so that one's first copies run under another's products.
+// Small rings, so that several CTAs share an SM and one's first copies run under another's
+// products (32-key tiles in twice the memory: 19.9 against 17.5 us at 64 sequences of up to
+// 1024 keys, d = 64; three stages: 29 against 26 us at 512 keys, d = 128).
 template <int DP, bool SHARE>
 struct Cfg {
-  static constexpr int kKeys = DP <= 128 ? 32 : 16;       // keys of a tile
   static constexpr uint32_t kTile = kKeys * DP * 2;       // one matrix of a tile
   static constexpr int W = SHARE || DP == 64 ? 4 : 2;
-  static constexpr int kStages = SHARE ? 6 : 3;
+  static constexpr int kStages = SHARE ? 6 : DP == 64 ? 3 : 2;
   static constexpr uint32_t kRing = kStages * 2 * kTile;
   static constexpr uint32_t kSmem = SHARE ? kRing : W * kRing;
   static_assert(SHARE || kSmem >= W * 16 * (DP + 8 + 2) * 4, "the join's sums");
@@ -66,7 +69,7 @@ template <int DP, bool HL, bool SHARE>
 __global__ void __launch_bounds__(Cfg<DP, SHARE>::W * 32) range_mma_kernel(const __grid_constant__ Params q) {
   using C = Cfg<DP, SHARE>;
   constexpr int NS = DP / 16, NT = DP / 8;                // k-steps of a score, column tiles
-  constexpr int NR = HL ? 1 : 2, KEYS = C::kKeys, KG = KEYS / 16;      // rows a thread, key groups
+  constexpr int NR = HL ? 1 : 2;                          // rows a thread
   constexpr int W = C::W, RB = 8 * NR * (SHARE ? W : 1), S = C::kStages;
   const int hk = blockIdx.y;
   // After a launch for the prefix the own ranges need nothing of it and start while it runs:
@@ -89,17 +92,17 @@ __global__ void __launch_bounds__(Cfg<DP, SHARE>::W * 32) range_mma_kernel(const
   const __nv_bfloat16* vp = (const __nv_bfloat16*)q.a.vp;
 
   // Where tile i's keys lie: the page (its number is loaded a tile ahead of its use) and row
-  // in it of one key a lane, or, where no group of 16 reaches over a page's end and rows are
-  // not padded, of the first key of the lane's group: then the group is one run of memory.
-  const bool flat = q.a.page % 16 == 0 && d == DP;
-  const int ntiles = (it.k1 - it.k0 + KEYS - 1) / KEYS;
+  // in it of one key a lane (lanes 0-15), or, where no tile reaches over a page's end and rows
+  // are not padded, of the tile's first key: then the tile is one run of memory.
+  const bool flat = q.a.page % kKeys == 0 && d == DP;
+  const int ntiles = (it.k1 - it.k0 + kKeys - 1) / kKeys;
   const int mine = SHARE ? ntiles : ntiles > warp ? (ntiles - warp + W - 1) / W : 0;
-  auto first_key = [&](int i) { return it.k0 + (SHARE ? i : warp + i * W) * KEYS; };
+  auto first_key = [&](int i) { return it.k0 + (SHARE ? i : warp + i * W) * kKeys; };
   struct Spot {
     int id, in;                                           // in < 0: no key
   };
   auto lookup = [&](int i) {
-    const int key = first_key(i) + (flat ? lane & (KEYS - 16) : lane & (KEYS - 1));
+    const int key = first_key(i) + (flat ? 0 : lane & 15);
     Spot s{0, -1};
     if (i < mine && key < it.k1) {
       const int pg = key / q.a.page;
@@ -120,26 +123,20 @@ __global__ void __launch_bounds__(Cfg<DP, SHARE>::W * 32) range_mma_kernel(const
         report(q.a.dev_status, DARK_ERR_INVALID_ARG);
     }
     if (flat) {
-      int64_t o[KG];
-      int live[KG];                                       // 16-byte pieces of the group
+      const int live = row < 0 ? 0 : (it.k1 - first_key(i)) * CH;      // 16-byte pieces
+      const int64_t o = row < 0 ? 0 : row * DP + me * 8;
 #pragma unroll
-      for (int kg = 0; kg < KG; ++kg) {
-        const int64_t base = KG > 1 ? __shfl_sync(0xffffffffu, row, 16 * kg) : row;
-        live[kg] = base < 0 ? 0 : (it.k1 - first_key(i) - 16 * kg) * CH;
-        o[kg] = base < 0 ? 0 : base * DP + me * 8;
-      }
-#pragma unroll
-      for (int n = 0; n < KEYS * CH / T; ++n) {
-        const int kg = n * T / (16 * CH), idx = n * T - kg * 16 * CH + me;
-        const bool ok = idx < live[kg];
-        const uint32_t to = tile_off<DP>(kg * 16 + idx / CH, idx % CH);
-        const int64_t from = ok ? o[kg] + (n * T - kg * 16 * CH) * 8 : 0;
+      for (int n = 0; n < kKeys * CH / T; ++n) {
+        const int idx = n * T + me;
+        const bool ok = idx < live;
+        const uint32_t to = tile_off<DP>(idx / CH, idx % CH);
+        const int64_t from = ok ? o + n * T * 8 : 0;
         cp16(k0 + to, kp + from, ok);
         cp16(v0 + to, vp + from, ok);
       }
     } else {
 #pragma unroll
-      for (int n = 0; n < KEYS * CH / T; ++n) {
+      for (int n = 0; n < kKeys * CH / T; ++n) {
         const int idx = n * T + me, r = idx / CH, c = idx % CH;
         const int64_t at = __shfl_sync(0xffffffffu, row, r);
         const bool ok = at >= 0 && c < chunks;
@@ -214,32 +211,30 @@ __global__ void __launch_bounds__(Cfg<DP, SHARE>::W * 32) range_mma_kernel(const
       cp_commit();
     }
     const uint32_t k0 = ring0 + (uint32_t)(i % S) * 2 * C::kTile, v0 = k0 + C::kTile;
-    float s[2 * KG][4];
+    float s[2][4];
 #pragma unroll
-    for (int n = 0; n < 2 * KG; ++n)
+    for (int n = 0; n < 2; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
 #pragma unroll
-    for (int st = 0; st < NS; ++st)
+    for (int st = 0; st < NS; ++st) {
+      uint32_t b[4];
+      ldsm4(b, k0 + tile_off<DP>((lg >> 1) * 8 + lr, 2 * st + (lg & 1)));
 #pragma unroll
-      for (int kg = 0; kg < KG; ++kg) {
-        uint32_t b[4];
-        ldsm4(b, k0 + tile_off<DP>(kg * 16 + (lg >> 1) * 8 + lr, 2 * st + (lg & 1)));
-#pragma unroll
-        for (int h = 0; h < NH; ++h) {
-          mma16816_bf16(s[2 * kg], ya[h][st], b[0], b[1]);
-          mma16816_bf16(s[2 * kg + 1], ya[h][st], b[2], b[3]);
-        }
+      for (int h = 0; h < NH; ++h) {
+        mma16816_bf16(s[0], ya[h][st], b[0], b[1]);
+        mma16816_bf16(s[1], ya[h][st], b[2], b[3]);
       }
+    }
     const int tile0 = first_key(i), key0 = tile0 + 2 * t;
-    uint32_t pa[KG][4];
+    uint32_t pa[4];
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
-      float v[4 * KG];                                    // keys key0 + 8 n + {0, 1} of row g + 8 r
+      float v[4];                                         // keys key0 + {0, 1, 8, 9} of row g + 8 r
       const int end = min(it.k1, lim[r]);
       float top = -INFINITY;
 #pragma unroll
-      for (int e = 0; e < 4 * KG; ++e) {
+      for (int e = 0; e < 4; ++e) {
         const float x = HL ? s[e >> 1][e & 1] + s[e >> 1][2 + (e & 1)] : s[e >> 1][2 * r + (e & 1)];
         v[e] = key0 + (e >> 1) * 8 + (e & 1) < end ? x : -INFINITY;
         top = fmaxf(top, v[e]);
@@ -263,52 +258,46 @@ __global__ void __launch_bounds__(Cfg<DP, SHARE>::W * 32) range_mma_kernel(const
       }
       const float m = ref[r] == -INFINITY ? 0.f : ref[r];
 #pragma unroll
-      for (int e = 0; e < 4 * KG; ++e) {
+      for (int e = 0; e < 4; ++e) {
         v[e] = tc::ex2(v[e] - m);
         l[r] += v[e];
       }
 #pragma unroll
-      for (int n = 0; n < 2 * KG; ++n) {                  // operand registers: rows g, g + 8 by keys 0, 8
-        uint32_t& first = pa[n >> 1][2 * (n & 1) + r];
+      for (int n = 0; n < 2; ++n) {                       // operand registers: rows g, g + 8 by keys 0, 8
+        uint32_t& first = pa[2 * n + r];
         first = tc::pack_bf16(v[2 * n], v[2 * n + 1]);
-        if (HL)
-          pa[n >> 1][2 * (n & 1) + 1] =
-              tc::pack_bf16(v[2 * n] - bf16_half(first, 0), v[2 * n + 1] - bf16_half(first, 1));
+        if (HL) pa[2 * n + 1] = tc::pack_bf16(v[2 * n] - bf16_half(first, 0), v[2 * n + 1] - bf16_half(first, 1));
       }
     }
     // A weight of 0 does not cancel an infinite or NaN value of a key that only other rows
     // see (causal, the last T - 1 keys): a tile with one adds its values key by key.
-    if (tile0 + KEYS > seen_by_all && tile_non_finite<DP, KEYS>(v0, lane)) {
-#pragma unroll
-      for (int kg = 0; kg < KG; ++kg)
+    if (tile0 + kKeys > seen_by_all && tile_non_finite<DP>(v0, lane)) {
 #pragma unroll 1
-        for (int kk = 0; kk < 16; ++kk) {
-          const int src = (lane & ~3) | ((kk & 7) >> 1), key = kg * 16 + kk;
+      for (int kk = 0; kk < kKeys; ++kk) {
+        const int src = (lane & ~3) | ((kk & 7) >> 1);
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {                   // (HL: the second is lo of the same row)
-            const uint32_t w = __shfl_sync(0xffffffffu, kk < 8 ? pa[kg][r] : pa[kg][2 + r], src);
-            if (tile0 + key >= min(it.k1, lim[HL ? 0 : r])) continue;
-            const float p = bf16_half(w, kk & 1);
+        for (int r = 0; r < 2; ++r) {                     // (HL: the second is lo of the same row)
+          const uint32_t w = __shfl_sync(0xffffffffu, kk < 8 ? pa[r] : pa[2 + r], src);
+          if (tile0 + kk >= min(it.k1, lim[HL ? 0 : r])) continue;
+          const float p = bf16_half(w, kk & 1);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              const uint32_t x = ld_shared_u32(v0 + tile_off<DP>(key, n) + 4 * t);
-              o[n][2 * r] = fmaf(p, bf16_half(x, 0), o[n][2 * r]);
-              o[n][2 * r + 1] = fmaf(p, bf16_half(x, 1), o[n][2 * r + 1]);
-            }
+          for (int n = 0; n < NT; ++n) {
+            const uint32_t x = ld_shared_u32(v0 + tile_off<DP>(kk, n) + 4 * t);
+            o[n][2 * r] = fmaf(p, bf16_half(x, 0), o[n][2 * r]);
+            o[n][2 * r + 1] = fmaf(p, bf16_half(x, 1), o[n][2 * r + 1]);
           }
         }
+      }
       if (!SHARE) __syncwarp();
       continue;
     }
 #pragma unroll
-    for (int kg = 0; kg < KG; ++kg)
-#pragma unroll
-      for (int n = 0; n < NT; n += 2) {
-        uint32_t b[4];
-        ldsm4_t(b, v0 + tile_off<DP>(kg * 16 + (lg & 1) * 8 + lr, n + (lg >> 1)));
-        mma16816_bf16(o[n], pa[kg], b[0], b[1]);
-        mma16816_bf16(o[n + 1], pa[kg], b[2], b[3]);
-      }
+    for (int n = 0; n < NT; n += 2) {
+      uint32_t b[4];
+      ldsm4_t(b, v0 + tile_off<DP>((lg & 1) * 8 + lr, n + (lg >> 1)));
+      mma16816_bf16(o[n], pa, b[0], b[1]);
+      mma16816_bf16(o[n + 1], pa, b[2], b[3]);
+    }
     if (!SHARE) __syncwarp();                             // the slot may be filled again
   }
   cp_wait<0>();
