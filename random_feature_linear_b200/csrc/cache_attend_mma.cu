@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(Cfg<DP, SHARE>::W * 32) range_mma_kernel(const
         report(q.a.dev_status, DARK_ERR_INVALID_ARG);
     }
     if (flat) {
-      const int live = row < 0 ? 0 : (it.k1 - first_key(i)) * CH;      // 16-byte pieces
+      const int live = row < 0 ? 0 : min(kKeys, it.k1 - first_key(i)) * CH;      // 16-byte pieces
       const int64_t o = row < 0 ? 0 : row * DP + me * 8;
 #pragma unroll
       for (int n = 0; n < kKeys * CH / T; ++n) {

@@ -172,6 +172,10 @@ CASES = {
     "page-7": dict(page=7, prefix=33, lens=(20, 131), T=2, causal=True),
     "shared-geometry": dict(shared_geom=True, prefix=64, lens=(40, 17)),
     "packed": dict(packed=True, T=3, prefix=64, lens=(40, 17), causal=True),
+    "many-sequences": dict(B=700, H=1, Hk=1, d=32, r=32, page=16, prefix=20,
+                           lens=tuple((7 * i) % 41 for i in range(700))),
+    "many-sequences-fp32": dict(dtype=F, B=700, H=1, Hk=1, d=32, r=32, page=16,
+                                lens=tuple((7 * i) % 41 for i in range(700))),
     "unequal": dict(B=6, lens=(1, 2500, 3, 64, 128, 7), page=32),
     "spare-pages": dict(spare_pages=5, prefix=30, lens=(40, 17)),
     "large-scores": dict(q_scale=12.0, prefix=200, lens=(100, 37)),

@@ -193,6 +193,39 @@ def test_backward_in_place_and_broadcast_cotangent(D, cuda_ok):
                                 ws=ws)
 
 
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("shift", [1, 2, 4])
+def test_misaligned_rows(D, cuda_ok, dtype, shift):
+    """Views whose rows begin at any element give the aligned views' bits."""
+    rng = np.random.default_rng(11)
+    B, H, L, d = 2, 3, 9, 64
+    gamma, rope = 1 + 0.1 * _t(rng, 1, d), D.dark_rope_init(d)
+
+    def off(t):
+        wide = torch.zeros(*t.shape[:3], d + 8, dtype=dtype, device="cuda")
+        v = wide[..., shift:shift + d]
+        v.copy_(t)
+        return v
+    q, dy = (_t(rng, B, H, L, d, dtype=dtype) for _ in range(2))
+    ws = D.alloc_qk_norm_rope_bwd_workspace(B, H, 0, L, d, "cuda")
+    res = []
+    for f in (lambda t: t.clone(), off):
+        x, g, y, dx = f(q), f(dy), f(torch.zeros_like(q)), f(torch.zeros_like(q))
+        dg = torch.empty_like(gamma)
+        D.dark_qk_norm_rope_fwd(x, None, y, None, gamma_q=gamma, rope=rope, pos0=3)
+        D.dark_qk_norm_rope_bwd(x, None, g, None, dx, None, gamma_q=gamma, dgamma_q=dg, rope=rope,
+                                pos0=3, ws=ws)
+        kp, vp = (torch.zeros(2, H, 16, d, dtype=dtype, device="cuda") for _ in range(2))
+        D.dark_kv_append(D.kv_cache(kp, vp), x, g,
+                         torch.arange(2, dtype=torch.int32, device="cuda")[:, None].contiguous(),
+                         torch.zeros(2, dtype=torch.int32, device="cuda"), gamma_k=gamma, rope=rope)
+        res.append([y, dx, dg, kp, vp])
+    half = 2 * HALF_STEP[dtype]                       # one step: other units, other sums' order
+    for a, b in zip(*res):
+        torch.testing.assert_close(a, b, rtol=half, atol=32 * U * 8)
+    assert torch.equal(res[0][4], res[1][4])
+
+
 def test_rows_around_the_result_stay(D, cuda_ok):
     """Results in a packed projection leave the values beside them alone."""
     rng = np.random.default_rng(6)
