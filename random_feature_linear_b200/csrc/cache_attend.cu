@@ -464,6 +464,7 @@ Plan make_plan(const CacheAttnArgs& a) {
   const size_t krows = (size_t)a.Hk * p.all;
   p.o_sched = take((size_t)p.cap * 16 + (size_t)(2 * a.B + 1) * 4);
   p.o_y = take(krows * p.dp * 4);
+  p.o_y16 = take(p.tc ? krows * p.dp * 2 : 0);
   p.o_pacc = take(a.prefix_len > 0 ? krows * p.p_splits * a.d * 4 : 0);
   p.o_pml = take(a.prefix_len > 0 ? krows * p.p_splits * 8 : 0);
   p.o_oacc = take((size_t)a.Hk * p.cap * p.rows * a.d * 4);

@@ -27,7 +27,7 @@ struct Plan {
   int p_splits, p_chunk;                  // ranges of the prefix, keys of a range
   int cap;                                // own ranges of all sequences, at most
   // byte offsets into the workspace
-  size_t o_sched, o_y, o_pacc, o_pml, o_oacc, o_oml, bytes;
+  size_t o_sched, o_y, o_y16, o_pacc, o_pml, o_oacc, o_oml, bytes;
 };
 
 // The cut of the own keys, written on the device from the sequences' lengths (one block

@@ -4,20 +4,25 @@
 //
 // A CTA takes one key range and up to RT tiles of 128 rows of one key head. Warps 0-3 (and
 // 4-7 for the second tile) turn scores into weights, a thread a row, 64 keys at a time;
-// warps 8 and 9 bring keys and values; one lane of warp 10 issues the products (a second
-// issuer, one a tile, measured 151 us against 141 at 1024 rows, 32768 keys, d = 128). S and O live
-// in TMEM; P replaces S there as bf16 and is the first operand of the second product, which
+// warp 8 brings keys and values, warps 9-12 convert the keys; one lane of warp 13 issues the
+// products (a second issuer, one a tile, measured 151 us against 141 at 1024 rows, 32768 keys,
+// d = 128). S and O live in TMEM; P replaces S there as bf16 and is the first operand of the second product, which
 // starts on the first 64 keys while the others are weighed. While one tile's scores are
 // exponentiated the other tile's products run.
 //
-// Queries are hi + lo in bf16 (one bf16 alone doubled the error of the result: 3.7e-3 against
-// 1.7e-3 of its size at 32768 keys), so that the first product has two parts; weights are
-// rounded to bf16, a smaller error than the result's own rounding; scores, sums and exponents
-// are fp32. Whole tiles of keys and values come by tensor copies of as many rows as
-// divide both the page and the tile (8 at least); tiles that end inside the range's last page, and pages
-// of other sizes, by 16-byte asynchronous copies with zeros behind the end (stale rows of a
-// page may hold anything, and a weight of 0 does not cancel an infinity). Those take about
-// 2000 cycles to issue a 128 x 128 tile, twice the products' time.
+// Queries are rounded to fp16 and the keys converted to it in shared memory (bf16 keys are
+// exact in fp16 between 2^-17 and 65504; anything larger is reported). bf16 queries (2^-9
+// instead of 2^-12 relative) doubled the error of the result: 3.7e-3 of its size against
+// 1.7e-3 at 32768 keys; hi + lo in bf16 keeps it but costs half as many products again (242 us
+// against 214 at 1024 rows of 8 heads, 32768 keys, d = 128; 35.5 against 36.7 at 64 rows, 4096
+// keys, d = 64, where the conversion of a CTA's few tiles shows). Weights are rounded to bf16;
+// scores, sums and exponents are fp32.
+//
+// Whole tiles of keys and values come by tensor copies of as many rows as divide both the
+// page and the tile (8 at least); tiles that end inside the range's last page, and pages of
+// other sizes, by 16-byte asynchronous copies with zeros behind the end (stale rows of a page
+// may hold anything, and a weight of 0 does not cancel an infinity). Those take about 2000
+// cycles to issue a 128 x 128 tile, twice the products' time.
 //
 // Bound by the two products (4 rows keys d operations) and the exponentials (rows keys)
 // alike: one 128 x 128 tile at d = 128 takes 1024 cycles of either unit.
@@ -34,17 +39,16 @@ namespace {
 using namespace tc;
 
 constexpr int kT = 128;                               // rows and keys of a tile
-constexpr int kSoftWarps = 8, kLoad = 64;             // weights; loading threads
-constexpr int kThreads = 32 * kSoftWarps + kLoad + 32;
+constexpr int kSoftWarps = 8, kConv = 128;            // weights; converting threads
+constexpr int kThreads = 32 * kSoftWarps + 32 + kConv + 32;
+constexpr int NK = 3, NV = 2;                         // slots of key and value tiles
 
 template <int DP>
 struct Tc {
   static constexpr int RT = 2;                        // row tiles (TMEM: RT (128 + DP) columns)
   static constexpr int kBlk = kT * 128;               // 128 rows of 64 columns
   static constexpr uint32_t kTile = DP / 64 * kBlk;   // 128 rows of DP columns, bf16
-  static constexpr int kSlots = DP == 64 ? 4 : 3;     // ring of key and value tiles
-  // queries: hi of the row tiles, then lo
-  static constexpr uint32_t oQ = 0, oRing = 2 * RT * kTile, oRows = oRing + kSlots * kTile;
+  static constexpr uint32_t oQ = 0, oK = RT * kTile, oV = oK + NK * kTile, oRows = oV + NV * kTile;
   static constexpr uint32_t oBar = oRows + kT * 8, kSmem = oBar + 256 + 1024;
   static constexpr uint32_t tS = 0, tO = RT * 128, kCols = 512;
   static_assert(tO + RT * DP <= kCols, "tmem");
@@ -104,8 +108,8 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
-// Whether any of the loading threads passes `bad`.
-__device__ __forceinline__ bool loaders_sync_or(bool bad) {
+// Whether any of the converting threads passes `bad`.
+__device__ __forceinline__ bool conv_sync_or(bool bad) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
@@ -113,55 +117,18 @@ __device__ __forceinline__ bool loaders_sync_or(bool bad) {
       "barrier.cta.red.or.pred q, 1, %2, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)bad), "n"(kLoad)
+      : "r"((uint32_t)bad), "n"(kConv)
       : "memory");
   return r != 0;
 }
-// Whether the phase with the given parity has completed (does not wait).
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.b32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
 struct Bars {
   uint64_t q, never, drain;
   // per row tile: scores, weights of the first and last 64 keys, the first's products, all sums
   uint64_t s[2], p[2][2], h[2], o[2];
-  uint64_t full[8], empty[8];             // ring slots
+  uint64_t kraw[NK], kfull[NK], kempty[NK], vfull[NV], vempty[NV];     // kraw: keys before conversion
   uint32_t tmem;
   int abort;
 };
-
-// 2^x for two values in the fused multiply-add units: x = n + f with n the nearest
-// whole number, 2^f by the polynomial of degree 3 with the least largest relative error on
-// [-1/2, 1/2] (Remez; 2^-13.7, against the 2^-9 of the rounding to bf16 that follows), n added
-// to the exponent. NaN stays out of range: its result is the largest finite number or NaN.
-__device__ __forceinline__ float2 ex2_fma(F2 v) {
-  float2 x = v.get();
-  // to [-126, 126]: results of 2^126 and more are made anew (kGuard)
-  asm("max.NaN.f32 %0, %0, 0fC2FC0000;\n\tmin.NaN.f32 %0, %0, 0f42FC0000;" : "+f"(x.x));
-  asm("max.NaN.f32 %0, %0, 0fC2FC0000;\n\tmin.NaN.f32 %0, %0, 0f42FC0000;" : "+f"(x.y));
-  const F2 y(x.x, x.y), big(12582912.f, 12582912.f);                   // 1.5 2^23
-  const F2 n = add2(y, big), f = fma2(add2(n, F2(-12582912.f)), F2(-1.f), y);
-  F2 p = fma2(F2(0.0551716691f), f, F2(0.242611122f));
-  p = fma2(p, f, F2(0.693260985f));
-  p = fma2(p, f, F2(0.999928074f));
-  const float2 pn = p.get(), nn = n.get();
-  return make_float2(__uint_as_float(__float_as_uint(pn.x) + (__float_as_uint(nn.x) << 23)),
-                     __uint_as_float(__float_as_uint(pn.y) + (__float_as_uint(nn.y) << 23)));
-}
-
-// The exponentials are shared between the special-function units (16 a cycle) and the
-// multiply-add units, one pair of kFma there: at d = 128 the products take 1024 cycles a tile
-// and the special functions alone would take as many.
-constexpr int kFma = 4;
 
 // A row's reference is the largest of its first 64 scores, and moves when the weights of 64
 // later ones sum up to more than this: bf16 and fp32 keep their relative precision at any
@@ -180,13 +147,8 @@ __device__ __forceinline__ float weigh(const uint32_t (&v)[64], uint32_t tp, flo
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
       const F2 x = add2(F2(__uint_as_float(v[32 * k + 2 * e]), __uint_as_float(v[32 * k + 2 * e + 1])), minus_r);
-      float2 p;
-      if (e % kFma == kFma - 1) {
-        p = ex2_fma(x);
-      } else {
-        p = x.get();
-        p = make_float2(ex2(p.x), ex2(p.y));
-      }
+      float2 p = x.get();
+      p = make_float2(ex2(p.x), ex2(p.y));
       if (TAIL) {
         const int c = c0 + 32 * k + 2 * e;
         p.x = c < end ? p.x : 0.f;
@@ -216,8 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1) range_tc_kernel(const __grid_cons
                                                                 const __grid_constant__ CUtensorMap tm_k,
                                                                 const __grid_constant__ CUtensorMap tm_v) {
   using C = Tc<DP>;
-  constexpr int RT = C::RT, S = C::kSlots, CH = DP / 8;
-  static_assert(S >= 3 && S <= 8, "ring");
+  constexpr int RT = C::RT, CH = DP / 8;
   static_assert(sizeof(Bars) <= 256, "barriers");
   const int hk = blockIdx.y;
   const Item it = item_of(q, blockIdx.x, hk, RT * kT, true, false);
@@ -233,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1) range_tc_kernel(const __grid_cons
   const int d = q.a.d, ks = (d + 15) / 16;            // steps of 16 columns
 
   if (tid == 0) {
-    mbar_init(&bar->q, kLoad);
+    mbar_init(&bar->q, kConv);
     mbar_init(&bar->never, 1);
     mbar_init(&bar->drain, 1);
     for (int i = 0; i < 2; ++i) {
@@ -243,9 +204,14 @@ __global__ void __launch_bounds__(kThreads, 1) range_tc_kernel(const __grid_cons
       mbar_init(&bar->h[i], 1);
       mbar_init(&bar->o[i], 1);
     }
-    for (int i = 0; i < S; ++i) {
-      mbar_init(&bar->full[i], kLoad);
-      mbar_init(&bar->empty[i], 1);
+    for (int i = 0; i < NK; ++i) {
+      mbar_init(&bar->kraw[i], 1);
+      mbar_init(&bar->kfull[i], kConv);
+      mbar_init(&bar->kempty[i], 1);
+    }
+    for (int i = 0; i < NV; ++i) {
+      mbar_init(&bar->vfull[i], 1);
+      mbar_init(&bar->vempty[i], 1);
     }
     bar->abort = 0;
     fence_mbar_init();
@@ -265,68 +231,76 @@ __global__ void __launch_bounds__(kThreads, 1) range_tc_kernel(const __grid_cons
     go = !*abort;
   }
 
-  if (go && warp >= kSoftWarps && warp < kSoftWarps + kLoad / 32) {
-    // ---- queries, then tiles K_0, V_0, K_1, V_1, ... through the ring; a copy is handed
-    // over when this thread's part of it has arrived (tensor copies count themselves). A
-    // thread that saw an abort goes on without copying: the barriers stay matched.
-    const int t = tid - 32 * kSoftWarps, c = t % CH;
-    const bool in = c < 2 * ks, has = c * 8 < d;      // (a last half step is zeros)
-    const int n = 2 * tiles, box = q.box_rows, nb = (d + 63) / 64;
-    const __nv_bfloat16* y = at<__nv_bfloat16>(q.a, q.p.o_y) + ((int64_t)hk * q.p.all + it.row0) * DP;
-    const int64_t lo = (int64_t)q.a.Hk * q.p.all * DP;
-    for (int r = t / CH; r < rts * kT; r += kLoad / CH) {
-      const uint32_t to = s0 + C::oQ + (r / kT) * C::kTile + kmajor_off(r % kT, c * 8, C::kBlk);
-      const __nv_bfloat16* src = y + (r < it.nrows ? (int64_t)r * DP + c * 8 : 0);
-      cp16(to, src, r < it.nrows);
-      cp16(to + RT * C::kTile, src + lo, r < it.nrows);
+  // tiles that come by tensor copies (the others, at the end of the last range or of pages of
+  // odd sizes, by the converting threads)
+  const int box = q.box_rows, whole = box > 0 ? (it.k1 - it.k0) / kT : 0;
+  if (go && warp == kSoftWarps) {
+    // ---- tensor copies K_0, V_0, K_1, V_1, ...
+    const int nb = (d + 63) / 64;
+    auto wait = [&](uint64_t* b, uint32_t parity) {
+      return (bool)__all_sync(0xffffffffu, wait_one(b, parity, abort, status));
+    };
+    auto copy = [&](const CUtensorMap* map, uint32_t dst, int key0, uint64_t* b) {
+      for (int x = lane; x < kT / box * nb; x += 32) {
+        const int r = x / nb * box, cb = x % nb, key = key0 + r, pg = key / q.a.page;
+        const int id = it.pages[pg];
+        const bool good = id >= 0 && id < q.a.pages;
+        if (!good) report(status, DARK_ERR_INVALID_ARG);
+        // a page outside the cache: outside the map, zeros
+        tma_load_3d(dst + cb * C::kBlk + r * 128, map, 64 * cb, key - pg * q.a.page,
+                    good ? id * q.a.Hk + hk : q.a.pages * q.a.Hk, b);
+      }
+      if (lane == 0) mbar_arrive_expect_tx(b, kT * 128 * nb);
+      __syncwarp();
+    };
+    int nk = 0, nv = 0;                               // copies issued
+    for (int j = 0; j < whole; ++j) {
+      const int key0 = it.k0 + j * kT, ik = j % NK, iv = j % NV;
+      if (j >= NK && !wait(&bar->kempty[ik], (j / NK - 1) & 1)) break;
+      copy(&tm_k, s0 + C::oK + ik * C::kTile, key0, &bar->kraw[ik]);
+      ++nk;
+      if (j >= NV && !wait(&bar->vempty[iv], (j / NV - 1) & 1)) break;
+      copy(&tm_v, s0 + C::oV + iv * C::kTile, key0, &bar->vfull[iv]);
+      ++nv;
     }
+    if (*abort && lane == 0) {                        // copies may be on their way
+      for (int j = max(0, nk - NK); j < nk; ++j) mbar_wait(&bar->kraw[j % NK], (j / NK) & 1, kWaitCycles / 8);
+      for (int j = max(0, nv - NV); j < nv; ++j) mbar_wait(&bar->vfull[j % NV], (j / NV) & 1, kWaitCycles / 8);
+    }
+    __syncwarp();
+  } else if (go && warp > kSoftWarps && warp < kSoftWarps + 1 + kConv / 32) {
+    // ---- queries; keys to fp16 in place; tiles without tensor copies. A thread that saw an
+    // abort goes on without copying: the barriers stay matched.
+    const int t = tid - 32 * (kSoftWarps + 1), c = t % CH;
+    const __half* y = at<__half>(q.a, q.p.o_y16) + ((int64_t)hk * q.p.all + it.row0) * DP;
+    for (int r = t / CH; r < rts * kT; r += kConv / CH)
+      cp16(s0 + C::oQ + (r / kT) * C::kTile + kmajor_off(r % kT, c * 8, C::kBlk),
+           y + (r < it.nrows ? (int64_t)r * DP + c * 8 : 0), r < it.nrows);
     cp_commit();
     int64_t* rows = reinterpret_cast<int64_t*>(sm + C::oRows);
-    int done = 0;                                     // copies handed over (this thread's part)
-    bool q_done = false, ok = true;
-    auto hand_over = [&](int pending) {               // copy `done`, `pending` groups behind it
-      if (pending == 0) cp_wait<0>();
-      else if (pending == 1) cp_wait<1>();
-      else cp_wait<2>();
-      fence_async_smem();
-      if (!q_done) mbar_arrive(&bar->q);              // (the queries' group came first)
-      q_done = true;
+    const bool in = c < 2 * ks, has = c * 8 < d;      // (a last half step is zeros)
+    bool ok = true;
+    auto fetch = [&](const void* pool, uint32_t dst) {
+      if (ok && in) {
+        const __nv_bfloat16* src = (const __nv_bfloat16*)pool + c * 8;
+#pragma unroll 4
+        for (int r = t / CH; r < kT; r += kConv / CH) {
+          const int64_t row = rows[r];
+          const bool live = row >= 0 && has;
+          cp16(dst + kmajor_off(r, c * 8, C::kBlk), src + (live ? row * d : 0), live);
+        }
+      }
+      cp_commit();
     };
-    for (int i = 0; i < n; ++i) {
-      const int slot = i % S, j = i / 2, key0 = it.k0 + j * kT;
-      const uint32_t dst = s0 + C::oRing + slot * C::kTile;
-      if (ok && i >= S) {
-        // while the slot is still read, hand over what has arrived
-        const uint32_t parity = (i / S - 1) & 1;
-        while (done < i && !mbar_test(&bar->empty[slot], parity)) {
-          hand_over(i - 1 - done);
-          mbar_arrive(&bar->full[done++ % S]);
-        }
-        ok = wait_one(&bar->empty[slot], parity, abort, status);
-      }
-      if (box > 0 && key0 + kT <= it.k1) {            // (then all copies before it were such)
-        if (ok) {
-          for (int x = t; x < kT / box * nb; x += kLoad) {
-            const int r = x / nb * box, cb = x % nb, key = key0 + r, pg = key / q.a.page;
-            const int id = it.pages[pg];
-            const bool good = id >= 0 && id < q.a.pages;
-            if (!good) report(status, DARK_ERR_INVALID_ARG);
-            // a page outside the cache: outside the map, zeros
-            tma_load_3d(dst + cb * C::kBlk + r * 128, i & 1 ? &tm_v : &tm_k, 64 * cb, key - pg * q.a.page,
-                        good ? id * q.a.Hk + hk : q.a.pages * q.a.Hk, &bar->full[slot]);
-          }
-        }
-        if (t == 0)
-          mbar_arrive_expect_tx(&bar->full[slot], kT * 128 * nb);
-        else
-          mbar_arrive(&bar->full[slot]);
-        ++done;
-        if (i == 1) hand_over(0);
-        continue;
-      }
-      if (!(i & 1)) {
-        loaders_sync_or(false);                       // the last tile's rows have been used
-        for (int k = t; k < kT; k += kLoad) {
+    __half2 top = __float2half2_rn(0.f);              // largest converted magnitude
+    for (int j = 0; j < tiles; ++j) {
+      const int ik = j % NK, iv = j % NV, key0 = it.k0 + j * kT;
+      const uint32_t tile = s0 + C::oK + ik * C::kTile;
+      const bool lone = j >= whole;
+      if (lone) {
+        if (ok && j >= NK) ok = wait_one(&bar->kempty[ik], (j / NK - 1) & 1, abort, status);
+        conv_sync_or(false);                          // the last tile's rows have been used
+        for (int k = t; k < kT; k += kConv) {
           const int key = key0 + k;
           int64_t row = -1;
           if (key < it.k1) {
@@ -335,89 +309,95 @@ __global__ void __launch_bounds__(kThreads, 1) range_tc_kernel(const __grid_cons
           }
           rows[k] = row;
         }
-        ok = !loaders_sync_or(!ok);
+        ok = !conv_sync_or(!ok);
+        fetch(q.a.kp, tile);
+        if (ok && j >= NV) ok = wait_one(&bar->vempty[iv], (j / NV - 1) & 1, abort, status);
+        fetch(q.a.vp, s0 + C::oV + iv * C::kTile);
+        cp_wait<1>();                                 // the keys (and the queries)
+      } else if (ok) {
+        ok = wait_one(&bar->kraw[ik], (j / NK) & 1, abort, status);
       }
       if (ok && in) {
-        const __nv_bfloat16* pool = (const __nv_bfloat16*)(i & 1 ? q.a.vp : q.a.kp) + c * 8;
 #pragma unroll 4
-        for (int r = t / CH; r < kT; r += kLoad / CH) {
-          const int64_t row = rows[r];
-          const bool live = row >= 0 && has;
-          cp16(dst + kmajor_off(r, c * 8, C::kBlk), pool + (live ? row * d : 0), live);
+        for (int r = t / CH; r < kT; r += kConv / CH) {
+          const uint32_t at = tile + kmajor_off(r, c * 8, C::kBlk);
+          const uint4 v = ld_shared_v4(at);
+          auto half2 = [&](uint32_t w) {
+            const __half2 h = __floats2half2_rn(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+            top = __hmax2(top, __habs2(h));
+            return *reinterpret_cast<const uint32_t*>(&h);
+          };
+          st_shared_v4(at, half2(v.x), half2(v.y), half2(v.z), half2(v.w));
         }
       }
-      cp_commit();
-      if (i - done >= 2) {
-        hand_over(i - done);
-        mbar_arrive(&bar->full[done++ % S]);
+      if (j == 0 && !lone) cp_wait<0>();              // the queries
+      fence_async_smem();
+      if (j == 0) mbar_arrive(&bar->q);
+      mbar_arrive(&bar->kfull[ik]);
+      if (lone) {
+        cp_wait<0>();
+        fence_async_smem();
+        conv_sync_or(false);
+        if (t == 0) mbar_arrive(&bar->vfull[iv]);
       }
     }
-    while (done < n) {
-      hand_over(n - 1 - done);
-      mbar_arrive(&bar->full[done++ % S]);
-    }
-    cp_wait<0>();
-    if (*abort && t == 0)                             // tensor copies may be on their way
-      for (int i = n > S ? n - S : 0; i < n; ++i) mbar_wait(&bar->full[i % S], (i / S) & 1, kWaitCycles / 8);
+    if (__hisinf(__low2half(top)) || __hisinf(__high2half(top))) report(status, DARK_ERR_NUMERIC);
   } else if (go && warp == kThreads / 32 - 1) {
     // ---- products: the warp stays together, one lane issues
     {
       const bool lead = elect_one();
-      const uint32_t id_s = idesc(kT, kT, false, false, false);
+      const uint32_t id_s = idesc(kT, kT, false, false, true);
       const uint32_t id_o = idesc(kT, 16 * ks, false, true, false);
       // operands' descriptors: steps add to the address field (one lane issues all products,
       // so that a few instructions a product count)
-      const uint64_t dq = sdesc(s0 + C::oQ, 16, 1024), dk = sdesc(s0 + C::oRing, 16, 1024);
-      const uint64_t dv = sdesc(s0 + C::oRing, C::kBlk, 1024);
-      auto scores = [&](int x, int i) {               // S_x = Y_x K^T, keys in ring copy i
+      const uint64_t dq = sdesc(s0 + C::oQ, 16, 1024), dk = sdesc(s0 + C::oK, 16, 1024);
+      const uint64_t dv = sdesc(s0 + C::oV, C::kBlk, 1024);
+      auto scores = [&](int x, int j) {               // S_x = Y_x K_j^T
         if (!lead) return;
-        const uint64_t a = dq + (uint32_t)(x * (C::kTile >> 4)), b = dk + (uint32_t)(i % S * (C::kTile >> 4));
+        const uint64_t a = dq + (uint32_t)(x * (C::kTile >> 4)), b = dk + (uint32_t)(j % NK * (C::kTile >> 4));
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int s = 0; s < DP / 16; ++s)
-            if (s < ks) {
-              const uint32_t step = (s / 4 * C::kBlk + s % 4 * 32) >> 4;
-              mma(tmem + C::tS + x * kT, a + h * (RT * C::kTile >> 4) + step, b + step, id_s, h + s > 0);
-            }
+        for (int s = 0; s < DP / 16; ++s)
+          if (s < ks) {
+            const uint32_t step = (s / 4 * C::kBlk + s % 4 * 32) >> 4;
+            mma(tmem + C::tS + x * kT, a + step, b + step, id_s, s > 0);
+          }
         mma_commit(&bar->s[x]);
-        if (x == rts - 1) mma_commit(&bar->empty[i % S]);
+        if (x == rts - 1) mma_commit(&bar->kempty[j % NK]);
       };
-      // O_x += P_x V over half of the keys, values in ring copy i
-      auto values = [&](int x, int i, int half, bool add) {
+      auto values = [&](int x, int j, int half, bool add) {       // O_x += P_x V_j over half of the keys
         if (!lead) return;
-        const uint64_t b = dv + (uint32_t)(i % S * (C::kTile >> 4) + half * (8192 >> 4));
+        const uint64_t b = dv + (uint32_t)(j % NV * (C::kTile >> 4) + half * (8192 >> 4));
         const uint32_t a = tmem + C::tS + x * kT + half * 32;
 #pragma unroll
         for (int s = 0; s < kT / 32; ++s)
           mma_ts(tmem + C::tO + x * DP, a + 8 * s, b + (s * 2048 >> 4), id_o, add || s > 0);
         if (half == 0) mma_commit(&bar->h[x]);
-        else if (x == rts - 1) mma_commit(&bar->empty[i % S]);
+        else if (x == rts - 1) mma_commit(&bar->vempty[j % NV]);
       };
       auto wait = [&](uint64_t* b, uint32_t parity) {
         return (bool)__all_sync(0xffffffffu, wait_one(b, parity, abort, status));
       };
-      bool ok = wait(&bar->q, 0) && wait(&bar->full[0], 0);
+      bool ok = wait(&bar->q, 0) && wait(&bar->kfull[0], 0);
       if (ok) {
         tc_fence_after();
         for (int x = 0; x < rts; ++x) scores(x, 0);
       }
       for (int j = 0; j < tiles && ok; ++j) {
-        const int iv = 2 * j + 1, ik = 2 * j + 2;
         const bool more = j + 1 < tiles;
-        ok = wait(&bar->full[iv % S], (iv / S) & 1);
+        ok = wait(&bar->vfull[j % NV], (j / NV) & 1);
         for (int x = 0; x < rts && ok; ++x) {
           ok = wait(&bar->p[x][0], j & 1);
           if (!ok) break;
           tc_fence_after();
-          values(x, iv, 0, j > 0);
+          values(x, j, 0, j > 0);
           // (the next keys' wait ahead of the weights', off the path to the scores)
-          ok = (!more || x > 0 || wait(&bar->full[ik % S], (ik / S) & 1)) && wait(&bar->p[x][1], j & 1);
+          ok = (!more || x > 0 || wait(&bar->kfull[(j + 1) % NK], ((j + 1) / NK) & 1)) &&
+               wait(&bar->p[x][1], j & 1);
           if (!ok) break;
           tc_fence_after();
-          values(x, iv, 1, true);
+          values(x, j, 1, true);
           if (more)
-            scores(x, ik);
+            scores(x, j + 1);
           else if (lead)
             mma_commit(&bar->o[x]);
         }
@@ -490,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1) range_tc_kernel(const __grid_cons
       tc_fence_after();
       // sums through shared memory (all tiles of the ring have been read): 32 rows of 32
       // columns a warp at a time, so that rows are written in runs of 128 bytes
-      float4* box = reinterpret_cast<float4*>(sm + C::oRing + warp * 4096);
+      float4* box = reinterpret_cast<float4*>(sm + C::oK + warp * 4096);
       const int row0 = x * kT + quad * 32;
       for (int c = 0; c < d; c += 32) {
         float o[32];

@@ -125,6 +125,7 @@ __global__ void __launch_bounds__(WARPS * 32) queries_mma_kernel(const __grid_co
   __syncthreads();
   const int gg = h % q.G, hk = h / q.G;
   const int64_t rows = (int64_t)q.a.Hk * q.p.all;
+  bool over = false;
   for (int idx = tid; idx < kRows * DP; idx += WARPS * 32) {
     const int row = idx / DP, c = idx - row * DP, k = n0 + row;
     if (k >= n) break;
@@ -132,9 +133,15 @@ __global__ void __launch_bounds__(WARPS * 32) queries_mma_kernel(const __grid_co
 #pragma unroll
     for (int x = 0; x < WARPS; ++x) v += sum[(x * 16 + row) * LD + c];
     const int b = k / q.a.T, tt = k - b * q.a.T;
-    store_query_hi_lo(at<__nv_bfloat16>(q.a, q.p.o_y), rows,
-                      (int64_t)hk * q.p.all + (b * q.G + gg) * q.a.T + tt, DP, c, v);
+    const int64_t to = (int64_t)hk * q.p.all + (b * q.G + gg) * q.a.T + tt;
+    store_query_hi_lo(at<__nv_bfloat16>(q.a, q.p.o_y), rows, to, DP, c, v);
+    if (q.p.tc) {
+      const __half y = __float2half_rn(v);
+      at<__half>(q.a, q.p.o_y16)[to * DP + c] = y;
+      over |= __hisinf(y) != 0;
+    }
   }
+  if (over) report(q.a.dev_status, DARK_ERR_NUMERIC);
 }
 
 template <int DP, int WARPS>

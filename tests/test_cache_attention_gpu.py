@@ -370,6 +370,38 @@ def test_queries_past_fp16_are_reported(D, cuda_ok):
     assert torch.isfinite(c.out[rest.cuda()]).all()
 
 
+@pytest.mark.parametrize("page", [16, 20])
+@pytest.mark.parametrize("j", [3, 599])
+@pytest.mark.parametrize("big", [1e5, -1e5])
+def test_prefix_keys_past_fp16_are_reported(D, cuda_ok, page, j, big):
+    """A key of one key head in a whole tile, or in the tile that ends inside a page; heads
+    that read the other key head keep their results."""
+    kw = dict(B=20, H=8, Hk=2, T=2, page=page, prefix=600, lens=tuple(range(2, 42, 2)))
+    ref = Call(D, **kw)
+    ref.run()
+    assert ref.status.item() == 0
+    c = Call(D, **kw)
+    c.kp[c.shared[j // page], 1, j % page, 7] = big
+    c.run()
+    assert c.status.item() == D.DARK_ERR_NUMERIC
+    assert torch.equal(c.out[:, :4], ref.out[:, :4])
+
+
+def test_queries_past_fp16_after_the_geometry_are_reported(D, cuda_ok):
+    c = Call(D, B=20, H=8, Hk=2, T=2, page=16, prefix=600, lens=tuple(range(2, 42, 2)))
+    c.geom.copy_(4 * torch.eye(64))
+    c.proj, c.wbuf = D.dark_make_projection(torch.zeros(1, 1, 64, device="cuda"), c.geom, 8,
+                                            c.proj.dtype)
+    ref = c.run().clone()
+    assert c.status.item() == 0
+    c.q[3, 2, 1, 5] = 6e4                              # times 16 / 8
+    c.run()
+    assert c.status.item() == D.DARK_ERR_NUMERIC
+    rest = torch.ones(20, 8, 2, dtype=torch.bool)
+    rest[3, 2, 1] = False
+    assert torch.equal(c.out[rest.cuda()], ref[rest.cuda()])
+
+
 @pytest.mark.parametrize("dtype", [BF, F])
 def test_calls_repeat_to_the_bit_and_share_no_state(D, cuda_ok, dtype):
     """Again, in a replayed graph on another stream, and two calls at once."""
