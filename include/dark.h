@@ -536,10 +536,12 @@ dark_status dark_kv_append(const dark_kv_cache* cache, const void* k, const int6
  * [0, max_pages * page_size] is clamped, and a page number outside the cache is not
  * followed (that sequence's outputs are then unspecified); both store
  * DARK_ERR_INVALID_ARG in dev_status. bf16 runs on the tensor cores when d is a multiple
- * of 8: queries go through the geometry in fp16 (|q| below 65504; a larger value is
- * reported as DARK_ERR_NUMERIC) and on as two bf16 parts, weights are rounded to bf16 or
- * finer before the products, sums and softmax statistics are fp32. Every other call is
- * computed in fp32 throughout. A non-finite output stores DARK_ERR_NUMERIC; infinities and
+ * of 8: queries go through the geometry in fp16 and on as two bf16 parts, or, with 64 rows
+ * of a key head and more (B * T * H / heads), d <= 128 and a prefix of 256 tokens and more,
+ * over that prefix in fp16 with its keys converted to fp16 (|q|, there also the query after
+ * the geometry and |k|, below 65504; a larger value is reported as DARK_ERR_NUMERIC);
+ * weights are rounded to bf16 or finer before the products, sums and softmax statistics are
+ * fp32. Every other call is computed in fp32 throughout. A non-finite output stores DARK_ERR_NUMERIC; infinities and
  * NaN in places that a query does not see do not reach it. Several lists may name the same
  * page. DARK_ERR_UNSUPPORTED: max_pages * page_size or prefix_len above 2^30,
  * B * T above 2^20, B * H * T above 2^24, sizes outside dark_make_projection's limits.

@@ -13,10 +13,11 @@
 // Queries are rounded to fp16 and the keys converted to it in shared memory (bf16 keys are
 // exact in fp16 between 2^-17 and 65504; anything larger is reported). bf16 queries (2^-9
 // instead of 2^-12 relative) doubled the error of the result: 3.7e-3 of its size against
-// 1.7e-3 at 32768 keys; hi + lo in bf16 keeps it but costs half as many products again (242 us
-// against 214 at 1024 rows of 8 heads, 32768 keys, d = 128; 35.5 against 36.7 at 64 rows, 4096
-// keys, d = 64, where the conversion of a CTA's few tiles shows). Weights are rounded to bf16;
-// scores, sums and exponents are fp32.
+// 1.7e-3 at 32768 keys; hi + lo in bf16 keeps it but costs half as many products again (whole
+// calls: 241 us against 206 at 1024 rows of 8 heads, 32768 keys, d = 128; 36.5 against 34.9 at
+// 64 rows, 4096 keys, d = 64). Four warps convert, one on each scheduler: two took 225 us, three
+// 213; conversion from registers, straight from global memory, 235. Weights are rounded to
+// bf16; scores, sums and exponents are fp32.
 //
 // Whole tiles of keys and values come by tensor copies of as many rows as divide both the
 // page and the tile (8 at least); tiles that end inside the range's last page, and pages of
@@ -24,8 +25,12 @@
 // may hold anything, and a weight of 0 does not cancel an infinity). Those take about 2000
 // cycles to issue a 128 x 128 tile, twice the products' time.
 //
-// Bound by the two products (4 rows keys d operations) and the exponentials (rows keys)
-// alike: one 128 x 128 tile at d = 128 takes 1024 cycles of either unit.
+// Bound by shared memory's bandwidth and the chain of a tile: the products alone (no
+// weights, no conversion) take 117 us of the launch's 153, the conversion 20, the
+// exponentials 16. All exponentials go to the special-function units: a quarter of them as
+// polynomials in the multiply-add units measured 212 against 206, since the converting warps
+// want the issue slots. Scores as two products of 64 keys, so that a half's weights overlap
+// the other half's products, measured 218: such a product costs as much as one of 128 keys.
 #include <math.h>
 
 #include "cache_attend_mma.cuh"

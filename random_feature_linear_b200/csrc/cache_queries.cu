@@ -6,7 +6,8 @@
 // first (the layout of accumulators and operands agree), and the warps' sums of y are
 // joined at the end. q is exact in fp16 above 2^-17 and below 65504 (larger values give
 // non-finite outputs, which the join reports), c_m M is fp16 as stored, and p goes as
-// hi + lo, so that y keeps 20 bits of p.
+// hi + lo, so that y keeps 20 bits of p. For prefixes on tcgen05 y is stored in fp16 as well
+// (past 65504: reported).
 //
 // Bound by latency: one read of M's rows (r d 2 bytes, shared by the CTAs of a head in L2).
 #include "cache_attend_mma.cuh"
