@@ -139,7 +139,10 @@ __global__ void __launch_bounds__(WARPS * 32) queries_mma_kernel(const __grid_co
     if (q.p.tc) {
       const __half y = __float2half_rn(v);
       at<__half>(q.a, q.p.o_y16)[to * DP + c] = y;
-      over |= __hisinf(y) != 0;
+      if (__hisinf(y)) {                                // (padding may hold anything)
+        const int64_t last = min((int64_t)q.a.lens[b], (int64_t)q.a.max_pages * q.a.page);
+        over |= !(q.a.flags & DARK_CAUSAL) || last - q.a.T + tt >= 0;
+      }
     }
   }
   if (over) report(q.a.dev_status, DARK_ERR_NUMERIC);

@@ -402,6 +402,25 @@ def test_queries_past_fp16_after_the_geometry_are_reported(D, cuda_ok):
     assert torch.equal(c.out[rest.cuda()], ref[rest.cuda()])
 
 
+@pytest.mark.parametrize("dtype,B,prefix", [(BF, 4, 50), (BF, 20, 600), (F, 4, 50)])
+@pytest.mark.parametrize("what", [6e4, "inf", "nan"])
+def test_padding_queries_may_hold_anything(D, cuda_ok, dtype, B, prefix, what):
+    lens = (0, 2, 4, 90) * (B // 4)
+    c = Call(D, dtype=dtype, B=B, H=8, Hk=2, T=5, lens=lens, causal=True, prefix=prefix)
+    c.geom.fill_(1.0)                                  # 6e4 becomes 64 * 6e4 / 8
+    c.proj, c.wbuf = D.dark_make_projection(torch.zeros(1, 1, 64, device="cuda"), c.geom, 8,
+                                            c.proj.dtype)
+    want = c.run().clone()
+    assert c.status.item() == 0
+    pad = torch.tensor([[n - 5 + t < 0 for t in range(5)] for n in lens], device="cuda")
+    c.q[pad[:, None].expand(B, 8, 5)] = 0.0
+    c.q[..., 5][pad[:, None].expand(B, 8, 5)] = float(what)
+    c.run()
+    assert c.status.item() == 0
+    assert torch.equal(c.out, want)
+    assert not c.out[pad[:, None].expand(B, 8, 5)].any()
+
+
 @pytest.mark.parametrize("dtype", [BF, F])
 def test_calls_repeat_to_the_bit_and_share_no_state(D, cuda_ok, dtype):
     """Again, in a replayed graph on another stream, and two calls at once."""
