@@ -79,31 +79,6 @@ __device__ __forceinline__ void tmem_st16_async(uint32_t taddr, const uint32_t (
       "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
-// 64 columns of this thread's TMEM lane. Loads and wait are one statement: the registers hold
-// nothing before the wait, and a copy that the compiler puts in between would take (or lose)
-// what is not there yet. (The outputs are written before the second address is read.)
-__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&v)[64]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
-      "%30, %31}, [%64];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, "
-      "%42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, "
-      "%60, %61, %62, %63}, [%65];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=&r"(v[0]), "=&r"(v[1]), "=&r"(v[2]), "=&r"(v[3]), "=&r"(v[4]), "=&r"(v[5]), "=&r"(v[6]),
-        "=&r"(v[7]), "=&r"(v[8]), "=&r"(v[9]), "=&r"(v[10]), "=&r"(v[11]), "=&r"(v[12]), "=&r"(v[13]),
-        "=&r"(v[14]), "=&r"(v[15]), "=&r"(v[16]), "=&r"(v[17]), "=&r"(v[18]), "=&r"(v[19]), "=&r"(v[20]),
-        "=&r"(v[21]), "=&r"(v[22]), "=&r"(v[23]), "=&r"(v[24]), "=&r"(v[25]), "=&r"(v[26]), "=&r"(v[27]),
-        "=&r"(v[28]), "=&r"(v[29]), "=&r"(v[30]), "=&r"(v[31]), "=&r"(v[32]), "=&r"(v[33]), "=&r"(v[34]),
-        "=&r"(v[35]), "=&r"(v[36]), "=&r"(v[37]), "=&r"(v[38]), "=&r"(v[39]), "=&r"(v[40]), "=&r"(v[41]),
-        "=&r"(v[42]), "=&r"(v[43]), "=&r"(v[44]), "=&r"(v[45]), "=&r"(v[46]), "=&r"(v[47]), "=&r"(v[48]),
-        "=&r"(v[49]), "=&r"(v[50]), "=&r"(v[51]), "=&r"(v[52]), "=&r"(v[53]), "=&r"(v[54]), "=&r"(v[55]),
-        "=&r"(v[56]), "=&r"(v[57]), "=&r"(v[58]), "=&r"(v[59]), "=&r"(v[60]), "=&r"(v[61]), "=&r"(v[62]),
-        "=&r"(v[63])
-      : "r"(taddr), "r"(taddr + 32)
-      : "memory");
-}
 // One lane of a converged warp, the same one every time.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -143,7 +118,7 @@ constexpr float kGuard = 4294967296.f;
 // Weights of 64 scores of a thread's row (keys c0 ... of the tile; TAIL: only keys below
 // `end` count) against the reference r, as bf16 into TMEM columns tp ..., and their sum.
 template <bool TAIL>
-__device__ __forceinline__ float weigh(const uint32_t (&v)[64], uint32_t tp, float r, int c0, int end) {
+__device__ __forceinline__ float weigh(const uint32_t (&v)[2][32], uint32_t tp, float r, int c0, int end) {
   const F2 minus_r(-r, -r);
   F2 sum[2] = {F2(0.f, 0.f), F2(0.f, 0.f)};
 #pragma unroll
@@ -151,7 +126,7 @@ __device__ __forceinline__ float weigh(const uint32_t (&v)[64], uint32_t tp, flo
     uint32_t w[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      const F2 x = add2(F2(__uint_as_float(v[32 * k + 2 * e]), __uint_as_float(v[32 * k + 2 * e + 1])), minus_r);
+      const F2 x = add2(F2(__uint_as_float(v[k][2 * e]), __uint_as_float(v[k][2 * e + 1])), minus_r);
       float2 p = x.get();
       p = make_float2(ex2(p.x), ex2(p.y));
       if (TAIL) {
@@ -167,12 +142,12 @@ __device__ __forceinline__ float weigh(const uint32_t (&v)[64], uint32_t tp, flo
   return sum[0].sum() + sum[1].sum();
 }
 template <bool TAIL>
-__device__ __forceinline__ float most(const uint32_t (&v)[64], int c0, int end) {
+__device__ __forceinline__ float most(const uint32_t (&v)[2][32], int c0, int end) {
   float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
   for (int e = 0; e < 64; e += 2) {
-    const float a = !TAIL || c0 + e < end ? __uint_as_float(v[e]) : -INFINITY;
-    const float b = !TAIL || c0 + e + 1 < end ? __uint_as_float(v[e + 1]) : -INFINITY;
+    const float a = !TAIL || c0 + e < end ? __uint_as_float(v[e / 32][e % 32]) : -INFINITY;
+    const float b = !TAIL || c0 + e + 1 < end ? __uint_as_float(v[e / 32][e % 32 + 1]) : -INFINITY;
     m[e / 2 & 3] = fmaxf(m[e / 2 & 3], fmaxf(a, b));
   }
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
@@ -427,8 +402,8 @@ __global__ void __launch_bounds__(kThreads, 1) range_tc_kernel(const __grid_cons
       for (int half = 0; half < 2; ++half) {
         const int c0 = 64 * half;
         const uint32_t tp = ts + 32 * half;           // (over scores that were read)
-        uint32_t v[64];
-        tmem_ld64(ts + c0, v);
+        uint32_t v[2][32];
+        tmem_ld_blocks(ts + c0, v);
         const bool tail = end < c0 + 64, first = j == 0 && half == 0;
         float lt = 0.f;
         auto weights = [&]() {

@@ -391,10 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (has_feat) {
       uint32_t a[32], b2[32];
       const uint32_t base = tmem + ((uint32_t)(quad * 32) << 16) + G::tD + 80 * half;
-      tmem_ld32_async(base, a);
-      tmem_ld32_async(base + 32, b2);
-      tmem_wait_ld(a);
-      tmem_wait_ld(b2);
+      tmem_ld64(base, a, b2);
 #pragma unroll
       for (int i = 0; i < 32; ++i) run[i] += __uint_as_float(a[i]);
 #pragma unroll

@@ -307,32 +307,71 @@ __host__ __device__ constexpr uint32_t kmajor_off(int row, int k, uint32_t kbloc
          (uint32_t)(k % 8) * 2u;
 }
 
-// Asynchronous variant: the 32 registers are written when tmem_wait_ld(r)
-// returns; the wait names them as in/out operands so that no use of them can
-// be scheduled before it. Lets one block of columns load while another is used.
-__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t (&r)[32]) {
+// Loads of several runs of columns. Loads and their wait are always one statement: a load's
+// registers hold nothing before the wait, so that a copy (or spill) which the compiler puts
+// between two statements would keep what is not there yet and free registers that the load
+// still writes. Operands tied through a second statement order the uses, not such copies.
+#define DARK_R0_31                                                                             \
+  "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, " \
+  "%20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31"
+#define DARK_R32_63                                                                             \
+  "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, " \
+  "%50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63"
+#define DARK_R64_95                                                                             \
+  "%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, %80, %81, " \
+  "%82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95"
+#define DARK_R96_127                                                                              \
+  "%96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, " \
+  "%112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127"
+#define DARK_OUT8(c, r, i)                                                                 \
+  c((r)[i]), c((r)[i + 1]), c((r)[i + 2]), c((r)[i + 3]), c((r)[i + 4]), c((r)[i + 5]), \
+      c((r)[i + 6]), c((r)[i + 7])
+#define DARK_OUT32(c, r) DARK_OUT8(c, r, 0), DARK_OUT8(c, r, 8), DARK_OUT8(c, r, 16), DARK_OUT8(c, r, 24)
+
+// 32 columns as raw words.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {" DARK_R0_31 "}, [%32];\n\t"
+               "tcgen05.wait::ld.sync.aligned;"
+               : DARK_OUT32("=r", v)
+               : "r"(taddr)
+               : "memory");
+}
+// 64 consecutive columns as two blocks of raw words.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&a)[32], uint32_t (&b)[32]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x64.b32 {" DARK_R0_31 ", " DARK_R32_63 "}, [%64];\n\t"
+               "tcgen05.wait::ld.sync.aligned;"
+               : DARK_OUT32("=r", a), DARK_OUT32("=r", b)
+               : "r"(taddr)
+               : "memory");
+}
+// Twice 16 consecutive columns.
+__device__ __forceinline__ void tmem_ld16x2(uint32_t ta, uint32_t tb, uint32_t (&a)[16], uint32_t (&b)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
-      "%30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr)
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, "
+      "%26, %27, %28, %29, %30, %31}, [%33];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : DARK_OUT8("=&r", a, 0), DARK_OUT8("=&r", a, 8), DARK_OUT8("=&r", b, 0), DARK_OUT8("=&r", b, 8)
+      : "r"(ta), "r"(tb)
       : "memory");
 }
-__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
-                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
-                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
-                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
-                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
-                 "+r"(r[30]), "+r"(r[31])
-               :
-               : "memory");
+// N blocks of 32 consecutive columns.
+template <int N>
+__device__ __forceinline__ void tmem_ld_blocks(uint32_t taddr, uint32_t (&v)[N][32]) {
+  static_assert(N == 1 || N == 2 || N == 4, "blocks");
+  if constexpr (N == 1)
+    tmem_ld32(taddr, v[0]);
+  else if constexpr (N == 2)
+    tmem_ld64(taddr, v[0], v[1]);
+  else
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x128.b32 {" DARK_R0_31 ", " DARK_R32_63 ", " DARK_R64_95
+                 ", " DARK_R96_127 "}, [%128];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : DARK_OUT32("=r", v[0]), DARK_OUT32("=r", v[1]), DARK_OUT32("=r", v[2]),
+                   DARK_OUT32("=r", v[3])
+                 : "r"(taddr)
+                 : "memory");
 }
 
 // exp2 of 32 values (minus a per-row offset) packed to bf16 and stored as four
@@ -353,24 +392,21 @@ __device__ __forceinline__ void exp2_pack_store32(const uint32_t (&r)[32], float
   }
 }
 
-// Columns [f_begin, f_end) of this thread's TMEM lane (32 at a time, the next
-// block's load in flight while the current one is exponentiated and stored).
+// Columns [f_begin, f_end) of this thread's TMEM lane (a multiple of 32), 64 at a time.
 __device__ __forceinline__ void exp2_rows_to_smem(uint32_t lane_taddr, int f_begin, int f_end,
                                                   float offset, bool zero, uint32_t tile, int row) {
-  uint32_t a[32], b[32];
-  tmem_ld32_async(lane_taddr + f_begin, a);
-  tmem_wait_ld(a);
+  int f0 = f_begin;
 #pragma unroll 1
-  for (int f0 = f_begin; f0 < f_end; f0 += 64) {
-    const bool more_b = f0 + 32 < f_end, more_a = f0 + 64 < f_end;
-    if (more_b) tmem_ld32_async(lane_taddr + f0 + 32, b);
+  for (; f0 + 64 <= f_end; f0 += 64) {
+    uint32_t a[32], b[32];
+    tmem_ld64(lane_taddr + f0, a, b);
     exp2_pack_store32(a, offset, zero, tile, row, f0);
-    if (!more_b) break;
-    tmem_wait_ld(b);
-    if (more_a) tmem_ld32_async(lane_taddr + f0 + 64, a);
     exp2_pack_store32(b, offset, zero, tile, row, f0 + 32);
-    if (!more_a) break;
-    tmem_wait_ld(a);
+  }
+  if (f0 < f_end) {
+    uint32_t a[32];
+    tmem_ld32(lane_taddr + f0, a);
+    exp2_pack_store32(a, offset, zero, tile, row, f0);
   }
 }
 

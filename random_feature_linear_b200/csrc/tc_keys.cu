@@ -339,10 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (c_run > -INFINITY) nrm += c_run;
       }
       uint32_t fv[NH][32], pk[NH][16];
-#pragma unroll
-      for (int q = 0; q < NH; ++q) tmem_ld32_async(lane_tm + G::tP + f_r0 + 32 * q, fv[q]);
-#pragma unroll
-      for (int q = 0; q < NH; ++q) tmem_wait_ld(fv[q]);
+      tmem_ld_blocks(lane_tm + G::tP + f_r0, fv);
       tc_fence_before();
       warp_arrive(bar_ffreeA);
 #pragma unroll
@@ -371,10 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = epi_wait(bar_ffullB, i & 1, abort_flag, p.dev_status))) break;
         tc_fence_after();
       }
-#pragma unroll
-      for (int q = 0; q < NH; ++q) tmem_ld32_async(lane_tm + G::tP + f_r1 + 32 * q, fv[q]);
-#pragma unroll
-      for (int q = 0; q < NH; ++q) tmem_wait_ld(fv[q]);
+      tmem_ld_blocks(lane_tm + G::tP + f_r1, fv);
       tc_fence_before();
       warp_arrive(bar_ffreeB);
 #pragma unroll

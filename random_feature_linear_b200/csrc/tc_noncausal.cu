@@ -386,13 +386,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t stage = s0 + G::oPsi + M_ * 128;
     auto store_out = [&](int i) {
       const int u = ub + i, bh = u / p.ntiles, t = u % p.ntiles, b = bh / p.H, h = bh % p.H;
-      uint32_t vh[32], vl[32];
-      tmem_ld32_async(lane_tm + G::tO + half * 32, vh);
-      tmem_ld32_async(lane_tm + G::tO + 64 + half * 32, vl);
-      // (each synchronous load waits for every load of the thread)
-      const float den = tmem_ld1(lane_tm + G::tO + 128) + tmem_ld1(lane_tm + G::tO + 129);
-      tmem_wait_ld(vh);
-      tmem_wait_ld(vl);
+      uint32_t vh[32], vl[32], vd[2];
+      asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {" DARK_R0_31 "}, [%66];\n\t"
+                   "tcgen05.ld.sync.aligned.32x32b.x32.b32 {" DARK_R32_63 "}, [%67];\n\t"
+                   "tcgen05.ld.sync.aligned.32x32b.x2.b32 {%64, %65}, [%68];\n\t"
+                   "tcgen05.wait::ld.sync.aligned;"
+                   : DARK_OUT32("=&r", vh), DARK_OUT32("=&r", vl), "=&r"(vd[0]), "=&r"(vd[1])
+                   : "r"(lane_tm + G::tO + half * 32), "r"(lane_tm + G::tO + 64 + half * 32),
+                     "r"(lane_tm + G::tO + 128)
+                   : "memory");
+      const float den = __uint_as_float(vd[0]) + __uint_as_float(vd[1]);
       const int tok = t * kT + row;
       const bool live = tok < p.L && (p.qmask == nullptr || p.qmask[(size_t)b * p.L + tok] != 0);
       const float inv = live && den > 0.f ? 1.f / den : 0.f;
@@ -444,10 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // ---- pass 0 (part A)
       uint32_t fv[NH][32], pk[NH][16];
-#pragma unroll
-      for (int q = 0; q < NH; ++q) tmem_ld32_async(lane_tm + G::tP + f_r0 + 32 * q, fv[q]);
-#pragma unroll
-      for (int q = 0; q < NH; ++q) tmem_wait_ld(fv[q]);
+      tmem_ld_blocks(lane_tm + G::tP + f_r0, fv);
       tc_fence_before();
       warp_arrive(bar_ffreeA);
 #pragma unroll
@@ -465,10 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = epi_wait(bar_ffullB, i & 1, abort_flag, p.dev_status))) break;
         tc_fence_after();
       }
-#pragma unroll
-      for (int q = 0; q < NH; ++q) tmem_ld32_async(lane_tm + G::tP + f_r1 + 32 * q, fv[q]);
-#pragma unroll
-      for (int q = 0; q < NH; ++q) tmem_wait_ld(fv[q]);
+      tmem_ld_blocks(lane_tm + G::tP + f_r1, fv);
       tc_fence_before();
       warp_arrive(bar_ffreeB);
 #pragma unroll

@@ -432,10 +432,7 @@ __global__ void __launch_bounds__(kThreadsF, 1)
         if (!(ok = epi_wait(bar_ffull, nblk & 1, abort_flag, p.dev_status))) break;
         tc_fence_after();
         uint32_t v[4][32];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_ld32_async(lane_tm + G::tF + 128 * half + 32 * q, v[q]);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_wait_ld(v[q]);
+        tmem_ld_blocks(lane_tm + G::tF + 128 * half, v);
         tc_fence_before();
         warp_arrive(bar_ffree);
         if (MODE == kStats) {
@@ -539,10 +536,7 @@ __global__ void __launch_bounds__(kThreadsF, 1)
       tc_fence_after();
       {
         uint32_t a[2][32];
-        tmem_ld32_async(lane_tm + G::tN + 64 * half, a[0]);
-        tmem_ld32_async(lane_tm + G::tN + 64 * half + 32, a[1]);
-        tmem_wait_ld(a[0]);
-        tmem_wait_ld(a[1]);
+        tmem_ld_blocks(lane_tm + G::tN + 64 * half, a);
         float rs = 0.f;      // row sum of the rounded masked scores over this key half
 #pragma unroll
         for (int cc = 0; cc < 8; ++cc) {
@@ -1058,26 +1052,25 @@ __global__ void __launch_bounds__(kThreadsV, 1)
       if (c > 0 && !(ok = grp_wait(grp, bar_ds + t, (c - 1) & 1, abort_flag, p.dev_status))) return false;
       tc_fence_after();
       // this thread: feature hrow of half grp, value columns 64 colh .. 64 colh + 63
-      uint32_t a[2][32];
-      if (c > 0) {
-        tmem_ld32_async(lane_tm + 128 * t + 64 * colh, a[0]);
-        tmem_ld32_async(lane_tm + 128 * t + 64 * colh + 32, a[1]);
-        tmem_wait_ld(a[0]);
-        tmem_wait_ld(a[1]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) a[0][i] = a[1][i] = 0u;
-      }
+      uint32_t a[32];
       const uint32_t sS = s0 + G::oS + grp * 32768;
       const uint32_t rowoff = (uint32_t)(hrow >> 3) * 1024 + (uint32_t)(hrow & 7) * 128;
 #pragma unroll
       for (int cg = 0; cg < 8; ++cg) {
+        if (cg % 4 == 0) {
+          if (c > 0) {
+            tmem_ld32(lane_tm + 128 * t + 64 * colh + 8 * cg, a);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) a[i] = 0u;
+          }
+        }
         uint32_t hi4[4], lo4[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int i = 8 * cg + 2 * e;
-          const float x0 = __uint_as_float(a[i >> 5][i & 31]);
-          const float x1 = __uint_as_float(a[(i + 1) >> 5][(i + 1) & 31]);
+          const int i = 8 * (cg % 4) + 2 * e;
+          const float x0 = __uint_as_float(a[i]);
+          const float x1 = __uint_as_float(a[i + 1]);
           const __nv_bfloat162 hv = __floats2bfloat162_rn(x0, x1);
           const float2 hf = __bfloat1622float2(hv);
           hi4[e] = *reinterpret_cast<const uint32_t*>(&hv);
@@ -1166,18 +1159,14 @@ __global__ void __launch_bounds__(kThreadsV, 1)
       tc_fence_after();
       float num[64];
       {
-        uint32_t hi[2][32], lo[2][32];
-        tmem_ld32_async(lane_tm + G::tNum + 64 * colh, hi[0]);
-        tmem_ld32_async(lane_tm + G::tNum + 64 * colh + 32, hi[1]);
-        tmem_ld32_async(lane_tm + G::tNum + 128 + 64 * colh, lo[0]);
-        tmem_ld32_async(lane_tm + G::tNum + 128 + 64 * colh + 32, lo[1]);
-        tmem_wait_ld(hi[0]);
-        tmem_wait_ld(hi[1]);
-        tmem_wait_ld(lo[0]);
-        tmem_wait_ld(lo[1]);
+        // (in steps: all 128 registers at once cost spills)
 #pragma unroll
-        for (int i = 0; i < 64; ++i)
-          num[i] = __uint_as_float(hi[i >> 5][i & 31]) + __uint_as_float(lo[i >> 5][i & 31]);
+        for (int k = 0; k < 64; k += 16) {
+          uint32_t hi[16], lo[16];
+          tmem_ld16x2(lane_tm + G::tNum + 64 * colh + k, lane_tm + G::tNum + 128 + 64 * colh + k, hi, lo);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) num[k + i] = __uint_as_float(hi[i]) + __uint_as_float(lo[i]);
+        }
       }
       tc_fence_before();
       warp_arrive(bar_nfree);
@@ -1246,10 +1235,7 @@ __global__ void __launch_bounds__(kThreadsV, 1)
         tc_fence_after();
         for (int t = 0; t < G::NTC; ++t) {
           uint32_t a[2][32];
-          tmem_ld32_async(lane_tm + 128 * t + 64 * colh, a[0]);
-          tmem_ld32_async(lane_tm + 128 * t + 64 * colh + 32, a[1]);
-          tmem_wait_ld(a[0]);
-          tmem_wait_ld(a[1]);
+          tmem_ld_blocks(lane_tm + 128 * t + 64 * colh, a);
           const int feat = 128 * (ft0 + t) + row;
           float* kv = p.st_kv + ((size_t)bh * M_ + feat) * D_ + 128 * vb + 64 * colh;
 #pragma unroll
