@@ -72,17 +72,13 @@ __global__ void __launch_bounds__(Cfg<DP, SHARE>::W * 32) range_mma_kernel(const
   constexpr int NR = HL ? 1 : 2;                          // rows a thread
   constexpr int W = C::W, RB = 8 * NR * (SHARE ? W : 1), S = C::kStages;
   const int hk = blockIdx.y;
-  // After a launch for the prefix the own ranges need nothing of it and start while it runs:
-  // it began after the queries' launch had ended, so what that wrote is in L2 (read past L1).
-  // The wait at the end then makes this launch's end that of both, for the join.
-  const bool late = !SHARE && (q.p.tc || q.p.share);
-  if (!late) pdl_wait();
+  // The queries and the list of ranges come from an earlier launch. Where the prefix's launch lies
+  // in between, this waits for that one too (which had waited for the queries'): only the wait
+  // makes results visible, although the own ranges need nothing of the prefix's.
+  pdl_wait();
   pdl_launch();
   const Item it = item_of(q, blockIdx.x, hk, RB, SHARE || (q.a.prefix_len > 0 && !q.p.tc && !q.p.share), !SHARE);
-  if (!it.any) {
-    if (late) pdl_wait();
-    return;
-  }
+  if (!it.any) return;
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int r0 = SHARE ? warp * 8 * NR : 0;               // this warp's first row of the block
@@ -363,7 +359,6 @@ __global__ void __launch_bounds__(Cfg<DP, SHARE>::W * 32) range_mma_kernel(const
       it.ml[2 * row + 1] = lw;
     }
   }
-  if (late) pdl_wait();
 }
 
 template <int DP, bool HL, bool SHARE>
