@@ -430,8 +430,9 @@ dark_status dark_rope_init(dark_rope* rope, int dims, double base, double scale,
  * sums in fp32, rounded once.
  *   q, q_out     device [B][H][L][d] of dtype, element strides {b, h, l} (NULL =
  *                contiguous); q_out may be q itself with the same strides
- *   k, k_out     device [B][Hk][L][d], likewise; NULL with Hk = 0: queries only. q_out
- *                and k_out must not overlap.
+ *   k, k_out     device [B][Hk][L][d], likewise; NULL with Hk = 0: queries only. k_out
+ *                may be k itself with the same strides; otherwise results overlap neither
+ *                inputs nor each other (q_out = k, k_out = q and k_out = q_out are refused)
  *   gamma_q/k    device fp32 [heads_g][d], heads_g = 1 (one weight for all heads) or the
  *                tensor's head count; NULL: that tensor is rotated without a norm
  *   eps          > 0 where a weight is given
@@ -453,9 +454,10 @@ dark_status dark_qk_norm_rope_fwd(const void* q, const int64_t* q_strides, const
  * Backward pass of dark_qk_norm_rope_fwd: with dq_out, dk_out the gradients of its
  * results, writes dq, dk (of dtype) and dgamma_q, dgamma_k (fp32, of the weights' shape;
  * summed over tokens and, for a shared weight, over heads, in a fixed order). q, k are
- * the forward's inputs. dq may be dq_out itself with the same strides (and dk dk_out);
- * otherwise results overlap neither inputs nor each other. A weight and its gradient
- * are both given or both NULL.
+ * the forward's inputs. dq may be dq_out or q itself with the same strides (and dk dk_out or
+ * k); otherwise results overlap neither inputs nor each other (the same address with other
+ * strides, or of the other tensor, is refused). A weight and its gradient are both given or
+ * both NULL.
  *   ws, ws_bytes device workspace of dark_qk_norm_rope_bwd_workspace_bytes(...) bytes,
  *                256-byte aligned, no initial contents; one for every call in flight
  */

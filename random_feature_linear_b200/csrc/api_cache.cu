@@ -155,6 +155,8 @@ dark_status dark_qk_norm_rope_fwd(const void* q, const int64_t* q_strides, const
                                   int* dev_status, void* stream) {
   if (q == nullptr || q_out == nullptr) return DARK_ERR_INVALID_ARG;
   if (Hk > 0 && (k == nullptr || k_out == nullptr || k_out == q_out)) return DARK_ERR_INVALID_ARG;
+  // a warp stores heads of q while it still fetches heads of k (and CTAs run in any order)
+  if (Hk > 0 && (q_out == k || k_out == q)) return DARK_ERR_INVALID_ARG;
   dark::NormRopeArgs a;
   const dark_status st = norm_rope_args(a, gamma_q, heads_gq, gamma_k, heads_gk, eps, rope,
                                         positions, pos0, B, H, Hk, L, d, dtype, dev_status, stream);
@@ -199,6 +201,7 @@ dark_status dark_qk_norm_rope_bwd(const void* q, const int64_t* q_strides, const
     return DARK_ERR_INVALID_ARG;
   if (Hk > 0 && (k == nullptr || dk_out == nullptr || dk == nullptr || dk == dq))
     return DARK_ERR_INVALID_ARG;
+  if (Hk > 0 && (dq == k || dq == dk_out || dk == q || dk == dq_out)) return DARK_ERR_INVALID_ARG;
   dark::NormRopeArgs a;
   const dark_status st = norm_rope_args(a, gamma_q, heads_gq, gamma_k, heads_gk, eps, rope,
                                         positions, pos0, B, H, Hk, L, d, dtype, dev_status, stream);
@@ -219,7 +222,8 @@ dark_status dark_qk_norm_rope_bwd(const void* q, const int64_t* q_strides, const
       !take_strides(a.set[0].xs, q_strides, B, H, L, d, false) ||
       !take_strides(a.set[0].gs, dq_out_strides, B, H, L, d, false) ||
       !take_strides(a.set[0].ys, dq_strides, B, H, L, d, true) ||
-      !in_place_ok(dq_out, a.set[0].gs, dq, a.set[0].ys))
+      !in_place_ok(dq_out, a.set[0].gs, dq, a.set[0].ys) ||
+      !in_place_ok(q, a.set[0].xs, dq, a.set[0].ys))
     return DARK_ERR_INVALID_ARG;
   if (Hk > 0) {
     a.set[1].x = k;
@@ -230,7 +234,8 @@ dark_status dark_qk_norm_rope_bwd(const void* q, const int64_t* q_strides, const
         !take_strides(a.set[1].xs, k_strides, B, Hk, L, d, false) ||
         !take_strides(a.set[1].gs, dk_out_strides, B, Hk, L, d, false) ||
         !take_strides(a.set[1].ys, dk_strides, B, Hk, L, d, true) ||
-        !in_place_ok(dk_out, a.set[1].gs, dk, a.set[1].ys))
+        !in_place_ok(dk_out, a.set[1].gs, dk, a.set[1].ys) ||
+        !in_place_ok(k, a.set[1].xs, dk, a.set[1].ys))
       return DARK_ERR_INVALID_ARG;
   }
   return from_cuda(dark::launch_norm_rope_bwd(a));

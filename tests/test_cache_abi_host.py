@@ -97,6 +97,17 @@ def test_norm_rope_bwd_refuses(D, kw):
     assert _bwd(D, **kw) == D.DARK_ERR_INVALID_ARG
 
 
+def test_norm_rope_refuses_results_in_the_other_input(D):
+    """The other tensor's heads are still to be read when a warp stores its first results."""
+    assert _fwd(D, qo=K) == D.DARK_ERR_INVALID_ARG
+    assert _fwd(D, ko=Q) == D.DARK_ERR_INVALID_ARG
+    for kw in [dict(dq=K), dict(dq=P + 0x9000000), dict(dk=Q), dict(dk=P + 0x8000000)]:
+        assert _bwd(D, **kw) == D.DARK_ERR_INVALID_ARG
+    # the forward's own input, with other strides
+    assert _bwd(D, dq=Q, dqs=S3(2048, 64, 256)) == D.DARK_ERR_INVALID_ARG
+    assert _bwd(D, dk=K, dks=S3(1024, 64, 128)) == D.DARK_ERR_INVALID_ARG
+
+
 def test_norm_rope_bwd_workspace_query(D):
     f = D.dark_qk_norm_rope_bwd_workspace_bytes
     assert f(1, 1, 0, 1, 4) > 0 and f(2, 4, 2, 8, 64) % 256 == 0

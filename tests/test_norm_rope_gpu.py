@@ -193,6 +193,23 @@ def test_backward_in_place_and_broadcast_cotangent(D, cuda_ok):
                                 ws=ws)
 
 
+def test_backward_into_the_inputs(D, cuda_ok):
+    """dq and dk in the memory of q and k."""
+    rng = np.random.default_rng(15)
+    q, dq = (_t(rng, 2, 8, 400, 64, dtype=BF) for _ in range(2))
+    k, dk = (_t(rng, 2, 3, 400, 64, dtype=BF) for _ in range(2))
+    g, rope = [1 + 0.1 * _t(rng, n, 64) for n in (8, 1)], D.dark_rope_init(64)
+    ws = D.alloc_qk_norm_rope_bwd_workspace(2, 8, 3, 400, 64, "cuda")
+    res = []
+    for x, y in ((torch.empty_like(q), torch.empty_like(k)), (q, k)):
+        dg = [torch.empty_like(t) for t in g]
+        D.dark_qk_norm_rope_bwd(q, k, dq, dk, x, y, gamma_q=g[0], gamma_k=g[1], dgamma_q=dg[0],
+                                dgamma_k=dg[1], rope=rope, ws=ws)
+        res.append([x, y] + dg)
+    for a, b in zip(*res):
+        assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("dtype", [BF, F])
 @pytest.mark.parametrize("shift", [1, 2, 4])
 def test_misaligned_rows(D, cuda_ok, dtype, shift):
