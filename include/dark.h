@@ -532,7 +532,8 @@ dark_status dark_kv_append(const dark_kv_cache* cache, const void* k, const int6
  *                padding and gets a zero output. DARK_EXACT is accepted.
  *   ws, ws_bytes device workspace of dark_cache_attention_workspace_bytes(...) bytes,
  *                256-byte aligned, no initial contents; one for every call in flight (two
- *                captured graphs that may run at once need two)
+ *                captured graphs that may run at once need two). The query never falls as B, T
+ *                or prefix_len grow: the workspace of the largest call serves smaller ones
  * A query that sees no token gets a zero output. Tokens behind a sequence's length, and
  * pages that no list names, are not read into results. A length outside
  * [0, max_pages * page_size] is clamped, and a page number outside the cache is not

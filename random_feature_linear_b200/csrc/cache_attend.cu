@@ -486,6 +486,32 @@ Plan make_plan(const CacheAttnArgs& a) {
   return p;
 }
 
+// Bytes that no call with as many sequences, queries a sequence and prefix tokens, or fewer,
+// needs more of. (A plan alone may shrink as the call grows: more rows fill the GPU with
+// fewer ranges of the prefix, and 64 rows go by other tiles than 63.) Of the splits above:
+//  * p_splits <= want / pb + 1 with pb >= Hk max(1, all / prb): Hk all p_splits <= min(all, prb) want +
+//    Hk all; on tcgen05 p_splits <= 4 * 148 / blocks or 1 alike with 256-row blocks; and
+//    p_splits is at most the prefix's steps, or tiles, everywhere;
+//  * cap <= B + want_own / ob + 1 alike, with the row blocks of a sequence.
+// Each right-hand side grows with B, T and prefix_len.
+size_t bound_bytes(const CacheAttnArgs& a, const Plan& p) {
+  const size_t Hk = a.Hk, krows = Hk * p.all, rows = p.rows, all = p.all;
+  const size_t want = kPrefixCtas * 148, want_own = kOwnCtas * 148;
+  const size_t steps = ((size_t)a.prefix_len + kKeyStep - 1) / kKeyStep;
+  const size_t prb = p.mma && p.dp == 256 ? 32 : 64, rb = p.mma ? 16 : 64;
+  auto least = [](size_t x, size_t y) { return x < y ? x : y; };
+  auto most = [](size_t x, size_t y) { return x > y ? x : y; };
+  size_t part = least(least(all, prb) * want + krows, krows * steps);
+  if (p.mma && p.dp <= 128 && all >= 64 && a.prefix_len >= 256)
+    part = most(part, least(most(least(all, kTcRows) * 4 * 148, krows), krows * ((steps + 1) / 2)));
+  const size_t own = krows + least(rows, rb) * want_own + Hk * rows;
+  const size_t cap = a.B + (want_own + Hk - 1) / Hk;
+  const bool y16 = p.mma && p.dp <= 128 && all >= 64 && a.prefix_len >= 256;
+  return kWsHeader + align_up(cap * 16 + (2 * (size_t)a.B + 1) * 4, 256) + align_up(krows * p.dp * 4, 256) +
+         align_up(y16 ? krows * p.dp * 2 : 0, 256) + align_up(part * a.d * 4, 256) + align_up(part * 8, 256) +
+         align_up(own * a.d * 4, 256) + align_up(own * 8, 256);
+}
+
 template <typename T, int RB, int KT, int NT>
 cudaError_t launch_range(const Params& q, bool prefix, bool own) {
   static int smem_set[64];
@@ -542,7 +568,11 @@ cudaError_t launch_all(const Params& q) {
 }  // namespace
 }  // namespace cache
 
-size_t cache_attention_workspace_bytes(const CacheAttnArgs& a) { return cache::make_plan(a).bytes; }
+size_t cache_attention_workspace_bytes(const CacheAttnArgs& a) {
+  const cache::Plan p = cache::make_plan(a);
+  const size_t b = cache::bound_bytes(a, p);
+  return b > p.bytes ? b : p.bytes;
+}
 
 cudaError_t launch_cache_attention(const CacheAttnArgs& a) {
   cache::Params q;

@@ -622,7 +622,8 @@ def dark_cache_attention_workspace_bytes(proj: dark_projection, cache: dark_kv_c
 
 def alloc_cache_attention_workspace(proj: dark_projection, cache: dark_kv_cache, B: int, H: int,
                                     T: int, prefix_len: int, max_pages: int, device):
-    """A workspace of the size dark_cache_attention_workspace_bytes asks for."""
+    """A workspace of the size dark_cache_attention_workspace_bytes asks for; it serves calls of
+    fewer sequences, queries or prefix tokens too."""
     n = dark_cache_attention_workspace_bytes(proj, cache, B, H, T, prefix_len, max_pages)
     return torch.empty(max(n, WS_HEADER_BYTES), dtype=torch.uint8, device=device)
 

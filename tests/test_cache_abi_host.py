@@ -211,6 +211,25 @@ def test_attention_workspace_query(D):
     assert f(_proj(D), _cache(D), 2, 4, 3, 1 << 20, 4096) < (1 << 26)
 
 
+@pytest.mark.parametrize("d,heads,H,dtype", [(64, 8, 8, "BF16"), (128, 8, 32, "BF16"),
+                                             (256, 2, 8, "BF16"), (40, 2, 6, "F32"),
+                                             (36, 1, 8, "BF16")])
+def test_attention_workspace_of_the_largest_call_is_enough(D, d, heads, H, dtype):
+    """The query never falls as sequences, queries a sequence or prefix tokens are added."""
+    dt = getattr(D, "DARK_" + dtype)
+    proj, cache = _proj(D, heads=1, d=d, dtype=dt), _cache(D, heads=heads, d=d, dtype=dt)
+    f = lambda B, T, prefix: D.dark_cache_attention_workspace_bytes(proj, cache, B, H, T, prefix, 64)
+    Bs, Ts, prefixes = list(range(1, 66)) + [127, 128, 129, 500], [1, 2, 3, 8, 9, 70], \
+        [0, 1, 63, 64, 65, 255, 256, 257, 4096, 4097, 32768]
+    for T in Ts:
+        for prefix in prefixes:
+            sizes = [f(B, T, prefix) for B in Bs]
+            assert sizes == sorted(sizes), (T, prefix)
+    for B in Bs:
+        for sizes in [[f(B, T, 4096) for T in Ts], [f(B, 1, prefix) for prefix in prefixes]]:
+            assert sizes == sorted(sizes), B
+
+
 def test_binding_checks_tensors(D):
     q, k = torch.zeros(2, 4, 8, 64), torch.zeros(2, 2, 8, 64)
     ok = dict(gamma_q=torch.ones(64), eps=1e-6)

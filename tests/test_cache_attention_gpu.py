@@ -454,6 +454,17 @@ def test_calls_repeat_to_the_bit_and_share_no_state(D, cuda_ok, dtype):
     a.check()
 
 
+def test_a_workspace_serves_smaller_batches(D, cuda_ok):
+    """Sequences leave a batch one by one; its workspace stays."""
+    kw = dict(H=8, Hk=8, page=64, prefix=1000)
+    ws = None
+    for B in (64, 63, 33, 17, 8, 1):
+        c = Call(D, B=B, lens=tuple(3 * i for i in range(B)), **kw)
+        ws = c.ws if ws is None else ws
+        c.run(ws=ws)
+        c.check()
+
+
 def test_large_cache_offsets(D, cuda_ok):
     """Pages whose values lie past 2^32 elements of the pool."""
     d, page, Hk = 256, 128, 8
