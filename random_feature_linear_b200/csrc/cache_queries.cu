@@ -5,9 +5,11 @@
 // p_i = (c_m M)_i q are the first operand of the second product as they come out of the
 // first (the layout of accumulators and operands agree), and the warps' sums of y are
 // joined at the end. q is exact in fp16 above 2^-17 and below 65504 (larger values give
-// non-finite outputs, which the join reports), c_m M is fp16 as stored, and p goes as
-// hi + lo, so that y keeps 20 bits of p. For prefixes on tcgen05 y is stored in fp16 as well
-// (past 65504: reported).
+// non-finite outputs, which the join reports), c_m M is fp16 as stored, and p goes as hi + lo
+// in fp16, scaled by a power of two for each query, so that its largest |p_i| lies between 2^10
+// and 2^15 (the power follows a p_i past that): p may have any size, and y keeps 22 bits of every
+// p_i above 2^-13 of the largest (2^-35 of the largest below). For prefixes on tcgen05 y is stored in fp16 as well (past
+// 65504: reported).
 //
 // Bound by latency: one read of M's rows (r d 2 bytes, shared by the CTAs of a head in L2).
 #include "cache_attend_mma.cuh"
@@ -79,6 +81,8 @@ __global__ void __launch_bounds__(WARPS * 32) queries_mma_kernel(const __grid_co
   for (int k = 0; k < NT; ++k)
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[k][e] = 0.f;
+  // exponent fields of |2 p_i| (rows g, g + 8) that the scale puts at 2^10; o is y 2^(137 - ex)
+  int ex[2] = {15, 15};
   for (int i = 0; i < mine; ++i) {
     cp_wait<1>();
     __syncwarp();
@@ -91,10 +95,36 @@ __global__ void __launch_bounds__(WARPS * 32) queries_mma_kernel(const __grid_co
       mma16816_f16(p[0], a[s], b[0], b[1]);
       mma16816_f16(p[1], a[s], b[2], b[3]);
     }
+    int top[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float m = fmaxf(fmaxf(fabsf(p[0][2 * e]), fabsf(p[0][2 * e + 1])),
+                            fmaxf(fabsf(p[1][2 * e]), fabsf(p[1][2 * e + 1])));
+      top[e] = __float_as_int(2.f * m) >> 23;
+      top[e] = max(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
+      top[e] = max(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
+    }
+    if (i == 0) {
+      ex[0] = max(ex[0], top[0]);
+      ex[1] = max(ex[1], top[1]);
+    } else if (__any_sync(0xffffffffu, top[0] > ex[0] + 4 || top[1] > ex[1] + 4)) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int now = top[e] > ex[e] + 4 ? top[e] : ex[e], field = 127 + ex[e] - now;
+        const float f = __int_as_float(field > 0 ? field << 23 : 0);       // (2^-127 and less: 0)
+        ex[e] = now;
+#pragma unroll
+        for (int k = 0; k < NT; ++k) {
+          o[k][2 * e] *= f;
+          o[k][2 * e + 1] *= f;
+        }
+      }
+    }
     uint32_t hi[4], lo[4];                             // rows g, g + 8 by columns 2 t, 2 t + 8
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float x = 2.f * p[e >> 1][(e & 1) * 2], y = 2.f * p[e >> 1][(e & 1) * 2 + 1];
+      const float s = __int_as_float((265 - ex[e & 1]) << 23);             // 2 * 2^(137 - ex)
+      const float x = s * p[e >> 1][(e & 1) * 2], y = s * p[e >> 1][(e & 1) * 2 + 1];
       const __half2 hh = __floats2half2_rn(x, y);
       const __half2 ll = __floats2half2_rn(x - __low2float(hh), y - __high2float(hh));
       hi[e] = *reinterpret_cast<const uint32_t*>(&hh);
@@ -117,11 +147,12 @@ __global__ void __launch_bounds__(WARPS * 32) queries_mma_kernel(const __grid_co
   // the warps' sums, in order of the warps; rows 8 words apart from a multiple of the 32 banks
   constexpr int LD = DP + 8;
   float* sum = reinterpret_cast<float*>(smem);         // [warp][16][LD]
+  const float back[2] = {__int_as_float((ex[0] - 10) << 23), __int_as_float((ex[1] - 10) << 23)};
 #pragma unroll
   for (int k = 0; k < NT; ++k) {
     float* to = sum + (warp * 16 + g) * LD + 8 * k + 2 * t;
-    *reinterpret_cast<float2*>(to) = make_float2(o[k][0], o[k][1]);
-    *reinterpret_cast<float2*>(to + 8 * LD) = make_float2(o[k][2], o[k][3]);
+    *reinterpret_cast<float2*>(to) = make_float2(o[k][0] * back[0], o[k][1] * back[0]);
+    *reinterpret_cast<float2*>(to + 8 * LD) = make_float2(o[k][2] * back[1], o[k][3] * back[1]);
   }
   __syncthreads();
   const int gg = h % q.G, hk = h / q.G;

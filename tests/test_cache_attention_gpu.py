@@ -370,6 +370,41 @@ def test_queries_past_fp16_are_reported(D, cuda_ok):
     assert torch.isfinite(c.out[rest.cuda()]).all()
 
 
+@pytest.mark.parametrize("B,prefix,d", [(2, 20, 64), (20, 600, 64), (20, 600, 128), (2, 20, 256)])
+@pytest.mark.parametrize("rows", [1, 40])
+def test_geometry_products_past_fp16(D, cuda_ok, B, prefix, d, rows):
+    """M q passes 65504 where q and y = M^T M q / sqrt(d) do not: rows of 0.05 against queries of
+    6e4 (d 0.05 6e4 = 1.9e5 and more). One row of M alone, or several between rows of zeros."""
+    c = Call(D, B=B, H=8, Hk=2, T=2, d=d, r=48, prefix=prefix, lens=tuple(range(2, 2 + 2 * B, 2)))
+    c.geom.zero_()
+    c.geom[:, 47 if rows == 1 else slice(3, 48, 7)] = 0.05
+    c.proj, c.wbuf = D.dark_make_projection(torch.zeros(1, 1, 48, device="cuda"), c.geom, 8,
+                                            c.proj.dtype)
+    sign = torch.randint(0, 2, c.q.shape[:3], device="cuda",
+                         generator=torch.Generator("cuda").manual_seed(1)) * 2 - 1
+    c.q.copy_(6e4 * sign[..., None])
+    c.kp *= 2.0 ** -10                                 # scores of about 6 and more
+    c.run()
+    c.check()
+
+
+@pytest.mark.parametrize("dtype,B,T", [(BF, 2, 2), (BF, 2, 4), (BF, 8, 2), (F, 2, 2)])
+def test_small_geometries_keep_their_bits(D, cuda_ok, dtype, B, T):
+    """M = 2^-12 against keys of 2^24 gives the bits of M = 1: powers of two alone (c_m M stays a
+    normal fp16 number; M q, about 2^-13, does not lose its low bits)."""
+    outs = []
+    for e in (0, 12):
+        c = Call(D, dtype=dtype, B=B, H=8, Hk=2, T=T, prefix=200, lens=tuple(range(T, T + 2 * B, 2)))
+        c.geom.copy_(torch.eye(64) * 2.0 ** -e)
+        c.proj, c.wbuf = D.dark_make_projection(torch.zeros(1, 1, 64, device="cuda"), c.geom, 8,
+                                                c.proj.dtype)
+        c.kp *= 2.0 ** (2 * e)
+        c.run()
+        assert c.status.item() == 0
+        outs.append(c.out)
+    assert torch.equal(*outs)
+
+
 @pytest.mark.parametrize("page", [16, 20])
 @pytest.mark.parametrize("j", [3, 599])
 @pytest.mark.parametrize("big", [1e5, -1e5])
