@@ -343,6 +343,29 @@ def test_bad_lists_are_reported(D, cuda_ok, dtype):
     c.check()
 
 
+# few rows, a prefix that warps share, tcgen05 with tensor copies and with odd pages, fp32
+@pytest.mark.parametrize("dtype,B,d,page", [(BF, 2, 64, 16), (BF, 6, 64, 16), (BF, 20, 64, 16),
+                                            (BF, 20, 128, 64), (BF, 20, 64, 20), (BF, 20, 256, 16),
+                                            (F, 3, 64, 16), (F, 20, 40, 24)])
+@pytest.mark.parametrize("at", [0, 11, -1])
+def test_bad_prefix_pages_are_reported(D, cuda_ok, dtype, B, d, page, at):
+    """A page number outside the cache in the shared list is not followed, and the next call with
+    a right list is right."""
+    kw = dict(dtype=dtype, B=B, H=4, Hk=1, d=d, r=32, page=page, prefix=777,
+              lens=tuple(i % 40 for i in range(B)))
+    c = Call(D, **kw)
+    good = c.d_shared.clone()
+    for bad in (10 ** 6, -1, c.cache.pages, -2 ** 31, 2 ** 31 - 1):
+        c.d_shared.copy_(good)
+        c.d_shared[at] = bad
+        c.run()
+        assert c.status.item() == D.DARK_ERR_INVALID_ARG
+        c.status.zero_()
+    c.d_shared.copy_(good)
+    c.run()
+    c.check()
+
+
 @pytest.mark.parametrize("dtype", [BF, F])
 def test_lists_may_share_pages(D, cuda_ok, dtype):
     """Sequences with the same pages, and a prefix that is also a sequence's own."""

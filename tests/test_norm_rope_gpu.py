@@ -176,6 +176,46 @@ def test_backward(D, cuda_ok, name):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("per_head", [False, True])
+@pytest.mark.parametrize("dtype,H,Hk,d", [(BF, 7, 1, 256), (BF, 12, 4, 64), (F, 2, 1, 128)])
+def test_weight_gradients_of_many_tokens(D, cuda_ok, dtype, H, Hk, d, per_head):
+    """Spans of 511 tokens a CTA and more, up to 511 rows a lane, against fp64 sums on the GPU. A
+    lane's chain, 5 shuffles and 8 warps: below (511 + 13 + 80) u of the magnitudes' sum, with
+    32 u and more of it for the rows' own values, as above."""
+    L = 296 * 510 + 77
+    g = torch.Generator("cuda").manual_seed(2)
+    t = lambda *s: torch.randn(*s, generator=g, device="cuda", dtype=torch.float32)
+    q, dq, k, dk = (t(1, h, L, d).to(dtype) for h in (H, H, Hk, Hk))
+    gq, gk = (1 + 0.2 * t(h if per_head else 1, d) for h in (H, Hk))
+    outs = [torch.empty_like(x) for x in (q, k, gq, gk)]
+    rope = D.dark_rope_init(d)
+    ws = D.alloc_qk_norm_rope_bwd_workspace(1, H, Hk, L, d, "cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    D.dark_qk_norm_rope_bwd(q, k, dq, dk, outs[0], outs[1], gamma_q=gq, gamma_k=gk,
+                            dgamma_q=outs[2], dgamma_k=outs[3], rope=rope, eps=1e-5, ws=ws,
+                            dev_status=status)
+    assert status.item() == 0
+    pos = torch.arange(L, device="cuda", dtype=torch.float64)
+    ang = pos[:, None] * 1e4 ** (-2.0 * torch.arange(d // 2, device="cuda", dtype=torch.float64) / d)
+    c, s = ang.cos(), ang.sin()
+    for x, dy, dg in ((q, dq, outs[2]), (k, dk, outs[3])):
+        sums, mags = [], []
+        for h in range(x.shape[1]):
+            v, y = x[0, h].double(), dy[0, h].double()
+            n = v * (v.square().mean(-1, keepdim=True) + 1e-5).rsqrt()
+            a, b = y[:, :d // 2], y[:, d // 2:]
+            u = torch.cat([a * c + b * s, b * c - a * s], 1)
+            size = torch.hypot(a, b).repeat(1, 2)
+            sums.append((u * n).sum(0))
+            mags.append((size * n.abs()).sum(0))
+        ref, mag = torch.stack(sums), torch.stack(mags)
+        if not per_head:
+            ref, mag = ref.sum(0, keepdim=True), mag.sum(0, keepdim=True)
+        tol = (511 + 13 + 80) * U * mag + ref.abs() * U
+        worst = ((dg.double() - ref).abs() / tol).max().item()
+        assert worst <= 1.0, worst
+
+
 def test_backward_in_place_and_broadcast_cotangent(D, cuda_ok):
     rng = np.random.default_rng(5)
     q = _t(rng, 2, 3, 40, 64, dtype=BF)
