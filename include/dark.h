@@ -499,7 +499,8 @@ typedef struct dark_kv_cache {
  *                tokens (none if not positive); the others are not read
  *   positions    device int32 [B][T], or NULL: pos0 + lens[b] + t (pos0: the length of a
  *                prefix that is not part of the sequence's own pages)
- * Two sequences must not name the same page where either writes. A token whose place has
+ * k and v do not lie in the cache's pages. Two sequences must not name the same page where
+ * either writes. A token whose place has
  * no page (a negative length, a place past max_pages, a page number outside the cache) is
  * not written and stores DARK_ERR_INVALID_ARG in dev_status. Sizes as above;
  * max_pages * page_size <= 2^30.
@@ -521,6 +522,7 @@ dark_status dark_kv_append(const dark_kv_cache* cache, const void* k, const int6
  * h / (H / cache->heads) (H a multiple of the cache's heads).
  *   q, out       device [B][H][T][d] of the projection's (and cache's) dtype, strides
  *                {b, h, t} (NULL = contiguous)
+ *                (out may lie in the memory of q, with any strides)
  *   prefix_pages device int32 [ceil(prefix_len / page_size)]: the prefix's page list;
  *                unused with prefix_len = 0
  *   page_table   device int32 [B][max_pages]
@@ -539,12 +541,14 @@ dark_status dark_kv_append(const dark_kv_cache* cache, const void* k, const int6
  * [0, max_pages * page_size] is clamped, and a page number outside the cache is not
  * followed (that sequence's outputs are then unspecified); both store
  * DARK_ERR_INVALID_ARG in dev_status. bf16 runs on the tensor cores when d is a multiple
- * of 8: queries go through the geometry in fp16 and on as two bf16 parts, or, with 64 rows
- * of a key head and more (B * T * H / heads), d <= 128 and a prefix of 256 tokens and more,
- * over that prefix in fp16 with its keys converted to fp16 (|q|, there also the query after
- * the geometry and |k|, below 65504; a larger value is reported as DARK_ERR_NUMERIC);
- * weights are rounded to bf16 or finer before the products, sums and softmax statistics are
- * fp32. Every other call is computed in fp32 throughout. A non-finite output stores DARK_ERR_NUMERIC; infinities and
+ * of 8: queries go through the geometry in fp16 (exact between 2^-17 and 65504) and on as two
+ * bf16 parts, or, with 64 rows of a key head and more (B * T * H / heads), d <= 128 and a
+ * prefix of 256 tokens and more, over that prefix in fp16 with its keys converted to fp16
+ * (|q|, there also the query after the geometry and |k|, below 65504; a larger value is
+ * reported as DARK_ERR_NUMERIC); weights are rounded to bf16 or finer before the products,
+ * sums and softmax statistics are fp32. Every other call is computed in fp32 throughout. So
+ * the roundings, and the order of the sums, of one sequence's result follow the sizes of its
+ * call (B, T and prefix_len), not only the sequence. A non-finite output stores DARK_ERR_NUMERIC; infinities and
  * NaN in places that a query does not see do not reach it. Several lists may name the same
  * page. DARK_ERR_UNSUPPORTED: max_pages * page_size or prefix_len above 2^30,
  * B * T above 2^20, B * H * T above 2^24, sizes outside dark_make_projection's limits.

@@ -71,7 +71,7 @@ __device__ __forceinline__ uint32_t tile_off(int row, int c) {
 }
 
 // Queries for the tensor cores: y = hi + lo in bf16 (16 bits of significand together;
-// one bf16 alone would move the exponents by 2^-9 relative, as much again as the rounding
+// one bf16 alone would move the exponents by up to 2^-8 relative, as much again as the rounding
 // of the output). hi rows first, then all lo rows, dp columns each.
 __device__ __forceinline__ void store_query_hi_lo(__nv_bfloat16* y, int64_t nrows, int64_t row,
                                                   int dp, int c, float v) {

@@ -11,8 +11,8 @@
 // exponentiated the other tile's products run.
 //
 // Queries are rounded to fp16 and the keys converted to it in shared memory (bf16 keys are
-// exact in fp16 between 2^-17 and 65504; anything larger is reported). bf16 queries (2^-9
-// instead of 2^-12 relative) doubled the error of the result: 3.7e-3 of its size against
+// exact in fp16 between 2^-17 and 65504; anything larger is reported). bf16 queries (rounded
+// by up to 2^-8 instead of 2^-11) doubled the error of the result: 3.7e-3 of its size against
 // 1.7e-3 at 32768 keys; hi + lo in bf16 keeps it but costs half as many products again (whole
 // calls: 241 us against 206 at 1024 rows of 8 heads, 32768 keys, d = 128; 36.5 against 34.9 at
 // 64 rows, 4096 keys, d = 64). Four warps convert, one on each scheduler: two took 225 us, three

@@ -523,6 +523,18 @@ def test_a_workspace_serves_smaller_batches(D, cuda_ok):
         c.check()
 
 
+@pytest.mark.parametrize("dtype,B,prefix", [(BF, 2, 50), (BF, 20, 600), (F, 20, 50)])
+def test_results_in_the_queries(D, cuda_ok, dtype, B, prefix):
+    """out in the memory of q, with other strides as well."""
+    c = Call(D, dtype=dtype, B=B, H=8, Hk=2, T=3, prefix=prefix, lens=tuple(range(B)), causal=True)
+    want = c.run().clone()
+    q = c.q
+    for out in (lambda t: t, lambda t: t.view(B, 3, 8, 64).permute(0, 2, 1, 3)):
+        c.q = q.clone()
+        assert torch.equal(c.run(out=out(c.q)), want)
+    assert c.status.item() == 0
+
+
 def test_large_cache_offsets(D, cuda_ok):
     """Pages whose values lie past 2^32 elements of the pool."""
     d, page, Hk = 256, 128, 8
