@@ -456,6 +456,17 @@ Plan make_plan(const CacheAttnArgs& a) {
   p.all = a.B * p.rows;
   p.mma = a.dtype == DARK_BF16 && a.d % 8 == 0;
   p.dp = p.mma ? (a.d <= 64 ? 64 : a.d <= 128 ? 128 : 256) : a.d;
+  // The prefix's kernel. us of a captured call in a row of such calls, 8 key heads, 16 own keys,
+  // d = 64 / 128, by tcgen05 | by warps that share keys | in one launch with the own ranges:
+  //   32 rows,   512 keys  16.2 / 19.8 | 16.3 /  19.5 |  12.5 /  15.4
+  //   32 rows,  8192       20.9 / 25.6 | 23.3 /  29.9 |  24.4 /  36.1
+  //   48 rows, 32768       37.7 / 49.8 | 64.4 /  96.7 |  84.4 / 151.6
+  //   64 rows,   512       17.4 / 20.7 | 18.8 /  23.8 |  13.5 /  17.0
+  //   64 rows,  2048       17.8 / 21.8 | 20.5 /  27.1 |  19.1 /  26.8
+  //  256 rows,   512       21.4 / 27.8 | 22.7 /  33.4 |  20.9 /  29.2
+  // (d = 256, 32 rows: 30.5 | 24.6 at 512 keys and 36.5 | 42.7 at 4096 for the last two.) A launch of
+  // its own costs 4 to 5 us and is worth it from about 2^17 rows x keys on; tcgen05 would pay from
+  // 17 rows on as well, and is kept to 64 rows because it takes keys up to 65504 only.
   p.tc = p.mma && p.dp <= 128 && p.all >= 64 && a.prefix_len >= 256;
   p.share = p.mma && !p.tc && p.all > 16 && a.prefix_len > 0;
   // ranges: about as many CTAs (over key heads, row blocks and ranges) as run at once
@@ -563,7 +574,9 @@ cudaError_t launch_all(const Params& q) {
     if (e != cudaSuccess) return e;
   }
   const int64_t rows = (int64_t)q.a.Hk * q.p.all;
-  // a warp a row while that gives every SM about eight warps
+  // a warp a row while that gives every SM about eight warps (whole calls, 8 key heads, d = 64,
+  // prefix 2048: 128 rows 19.9 us with one warp and 20.1 with four, 256 rows 23.7 and 26.5;
+  // 16 rows 13.4 and 12.2)
   return rows >= 8 * num_sms()
              ? launch_dependent(join_kernel<T, 1>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, q.a.stream, q)
              : launch_dependent(join_kernel<T, 4>, dim3((unsigned)rows), dim3(128), 0, q.a.stream, q);

@@ -7,11 +7,13 @@
 namespace dark {
 namespace cache {
 
-// Rows that one CTA of the tensor-core range kernel takes at once.
+// Rows that one CTA of the tensor-core range kernel takes at once. Over 1024 own keys of 64
+// sequences, 4 key heads, d = 64: 12 rows take 28.2 us in blocks of 16 and 34.0 of 8, 32 rows 46.0
+// and 51.0 (d = 128: 12 rows 51.5 and 71.3, 20 rows 84.7 and 84.1, 64 rows 118.5 and 165.9).
 inline int mma_rows(int dp, int rows) { return dp <= 128 && rows > 8 ? 16 : 8; }
 cudaError_t launch_ranges_mma(const Params& q);
 
-// The prefix's ranges for more rows, which share the keys in a CTA.
+// The prefix's ranges for more rows, which share the keys in a CTA: 32 rows as hi + lo, or 64.
 inline int share_rows(int dp, int all) { return dp <= 128 && all > 32 ? 64 : 32; }
 cudaError_t launch_prefix_mma(const Params& q);
 

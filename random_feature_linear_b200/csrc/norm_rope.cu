@@ -704,8 +704,9 @@ cudaError_t launch_rows(const NormRopeArgs& a) {
   const int nh = a.set[0].heads + a.set[1].heads;
   const int64_t groups = ((int64_t)a.B * a.L + rows - 1) / rows;
   const int64_t x = (groups + kRowWarps - 1) / kRowWarps;
-  // all heads of a token in one warp (its angles are computed once), unless that leaves
-  // SMs without two CTAs
+  // all heads of a token in one warp (its angles are computed once), unless that leaves SMs
+  // without two CTAs: 64 tokens of 40 heads, d = 128, 3.5 us cut and 15.6 whole, 2048 tokens of
+  // 16 heads, d = 64, 4.7 and 7.8; a head a warp takes 41 us instead of 16.5 at 8192 tokens of 20
   int hchunk = nh;
   while (hchunk > 1 && x * ((nh + hchunk - 1) / hchunk) < 2 * num_sms()) hchunk = (hchunk + 1) / 2;
   while ((nh + hchunk - 1) / hchunk > 65535) hchunk *= 2;
