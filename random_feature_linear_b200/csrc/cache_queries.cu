@@ -8,8 +8,8 @@
 // non-finite outputs, which the join reports), c_m M is fp16 as stored, and p goes as hi + lo
 // in fp16, scaled by a power of two for each query, so that its largest |p_i| lies between 2^10
 // and 2^15 (the power follows a p_i past that): p may have any size, and y keeps 22 bits of every
-// p_i above 2^-13 of the largest (2^-35 of the largest below). For prefixes on tcgen05 y is stored in fp16 as well (past
-// 65504: reported).
+// p_i above 2^-13 of the largest (2^-35 of the largest below). For prefixes on tcgen05 y is
+// stored in fp16 as well (past 65504: reported).
 //
 // Bound by latency: one read of M's rows (r d 2 bytes, shared by the CTAs of a head in L2).
 #include "cache_attend_mma.cuh"

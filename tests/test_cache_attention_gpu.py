@@ -411,6 +411,20 @@ def test_geometry_products_past_fp16(D, cuda_ok, B, prefix, d, rows):
     c.check()
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("powers", [(-12, 0, 3, 3), (3, 0, -12, -12), (-40, -2, 1, 3), (-3, 2, -6, 3)])
+def test_geometries_of_rising_rows(D, cuda_ok, d, powers):
+    """M q of 256 rows that grow or shrink along them, by powers of two a quarter: a warp meets
+    several of them, and rows far below (or of zeros) first."""
+    c = Call(D, B=3, H=4, Hk=2, T=2, d=d, r=256, prefix=40, lens=(30, 2, 77), q_scale=0.5)
+    scale = torch.tensor(powers, device="cuda").repeat_interleave(64).double()
+    c.geom.mul_((2.0 ** scale).float()[:, None])
+    c.proj, c.wbuf = D.dark_make_projection(torch.zeros(1, 1, 256, device="cuda"), c.geom, 4,
+                                            c.proj.dtype)
+    c.run()
+    c.check()
+
+
 @pytest.mark.parametrize("dtype,B,T", [(BF, 2, 2), (BF, 2, 4), (BF, 8, 2), (F, 2, 2)])
 def test_small_geometries_keep_their_bits(D, cuda_ok, dtype, B, T):
     """M = 2^-12 against keys of 2^24 gives the bits of M = 1: powers of two alone (c_m M stays a
