@@ -457,7 +457,7 @@ dark_status dark_qk_norm_rope_fwd(const void* q, const int64_t* q_strides, const
  * the forward's inputs. dq may be dq_out or q itself with the same strides (and dk dk_out or
  * k); otherwise results overlap neither inputs nor each other (the same address with other
  * strides, or of the other tensor, is refused). A weight and its gradient are both given or
- * both NULL.
+ * both NULL; dgamma_k is NULL with Hk = 0.
  *   ws, ws_bytes device workspace of dark_qk_norm_rope_bwd_workspace_bytes(...) bytes,
  *                256-byte aligned, no initial contents; one for every call in flight
  */

@@ -208,6 +208,7 @@ dark_status dark_qk_norm_rope_bwd(const void* q, const int64_t* q_strides, const
   if (st != DARK_OK) return st;
   // a weight and its gradient come together
   if ((gamma_q == nullptr) != (dgamma_q == nullptr) || !aligned(dgamma_q, 4)) return DARK_ERR_INVALID_ARG;
+  if (Hk <= 0 && dgamma_k != nullptr) return DARK_ERR_INVALID_ARG;       // nothing would write it
   if (Hk > 0 && (((gamma_k == nullptr) != (dgamma_k == nullptr)) || !aligned(dgamma_k, 4) ||
                  (dgamma_k != nullptr && dgamma_k == dgamma_q)))
     return DARK_ERR_INVALID_ARG;

@@ -108,6 +108,12 @@ def test_norm_rope_refuses_results_in_the_other_input(D):
     assert _bwd(D, dk=K, dks=S3(1024, 64, 128)) == D.DARK_ERR_INVALID_ARG
 
 
+def test_norm_rope_bwd_refuses_a_gradient_without_its_tensor(D):
+    kw = dict(k=None, gko=None, dk=None, Hk=0)
+    assert _bwd(D, **kw) == D.DARK_ERR_INVALID_ARG
+    assert _bwd(D, gk=None, **kw) == D.DARK_ERR_INVALID_ARG
+
+
 def test_norm_rope_bwd_workspace_query(D):
     f = D.dark_qk_norm_rope_bwd_workspace_bytes
     assert f(1, 1, 0, 1, 4) > 0 and f(2, 4, 2, 8, 64) % 256 == 0
