@@ -109,7 +109,7 @@ def test_norm_rope_refuses_results_in_the_other_input(D):
 
 
 def test_norm_rope_bwd_refuses_a_gradient_without_its_tensor(D):
-    kw = dict(k=None, gko=None, dk=None, Hk=0)
+    kw = dict(k=None, gko=None, dk=None, Hk=0, n=1 << 30)
     assert _bwd(D, **kw) == D.DARK_ERR_INVALID_ARG
     assert _bwd(D, gk=None, **kw) == D.DARK_ERR_INVALID_ARG
 
